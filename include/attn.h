@@ -71,7 +71,8 @@ enum {
   ATTN_DEV_SEQLEN = 2,       /* seqlens_k[b] < T, > max_seqlen_k or beyond the cache capacity */
   ATTN_DEV_APPEND_RANGE = 4, /* kv_append position beyond the cache capacity / page table */
   ATTN_DEV_TIMEOUT = 8,      /* a bounded wait inside a kernel gave up (no fault, results invalid) */
-  ATTN_DEV_SCALE = 16        /* an FP8 cache scale was not a positive finite number */
+  ATTN_DEV_SCALE = 16,       /* an FP8 cache scale was not a positive finite number */
+  ATTN_DEV_POSITION = 32     /* a token's position was outside the angle table (qk_norm_rope and kin) */
 };
 
 /*
@@ -253,6 +254,180 @@ ATTN_API int kv_append_fp8(void* k_cache, void* v_cache, const void* k_new, cons
                            const float* v_scale, const int32_t* cache_lens, const int32_t* page_table,
                            int max_blocks_per_seq, int num_blocks, int cache_capacity, int B, int T, int Hkv, int d,
                            void* stream);
+
+/*
+ * attn_prefill_window -- attn_prefill with a causal sliding window and a few
+ * first tokens that stay visible: the query at position p sees key j when
+ * j <= p and (j > p - window or j < sinks), so its own position, the window - 1
+ * before it, and the first `sinks`.  The pages have no counterpart; the softmax
+ * and the LSE are attn_prefill's over the seen keys (every row sees itself).
+ *
+ *   window  >= 1 (a window of N or more is plain causal attention)
+ *   sinks   >= 0
+ *   everything else as for attn_prefill
+ * The work grows with N * (window + sinks), not N^2: K/V tiles that no row of a
+ * query block sees are never read.
+ * Errors: attn_prefill's, ATTN_ERR_INVALID_ARG for window or sinks out of range, and
+ * ATTN_ERR_UNSUPPORTED for N above 2^30.
+ */
+ATTN_API int attn_prefill_window(const void* q, const void* k, const void* v, void* o, int o_dtype, float* lse, int B,
+                                 int Hq, int Hkv, int N, int d, float scale, int window, int sinks, void* stream);
+
+/*
+ * attn_prefill_cache_window -- attn_prefill_cache (causal) with the mask of
+ * attn_prefill_window; positions are those in the cache: query i of sequence b is
+ * at position seqlens_k[b] - Nq + i.  Page-table entries of blocks that lie wholly
+ * between the sinks and the first query's window are not read: their blocks may
+ * have been given back and their entries may hold anything.  A cache capacity (or
+ * max_blocks_per_seq * 16) above 2^30 is ATTN_ERR_UNSUPPORTED.
+ */
+ATTN_API int attn_prefill_cache_window(const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* seqlens_k, const int32_t* page_table, int max_blocks_per_seq,
+                                       int num_blocks, int cache_capacity, void* o, int o_dtype, float* lse, int B,
+                                       int Nq, int Hq, int Hkv, int d, float scale, int window, int sinks,
+                                       void* stream);
+
+/* Workspace bytes of attn_decode_window and attn_decode_window_fp8; 0 for invalid sizes. */
+ATTN_API size_t attn_decode_window_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int max_seqlen_k, int window,
+                                                   int sinks, int num_splits);
+
+/*
+ * attn_decode_window, attn_decode_window_fp8 -- attn_decode / attn_decode_fp8
+ * (causal) with the mask of attn_prefill_window: token t of T is at position
+ * p = seqlens_k[b] - T + t.  Only the blocks holding keys that some token of the
+ * call sees are read (16-token granularity in both cache layouts), so a step costs
+ * about sinks + window + T keys per sequence whatever its length; page-table
+ * entries between the sinks' blocks and the first token's window are not read.
+ * Arguments, kernels, length rules and errors as for attn_decode /
+ * attn_decode_fp8, with attn_decode_window_workspace_bytes for the workspace;
+ * num_splits counts chunks of the seen keys.
+ */
+ATTN_API int attn_decode_window(const void* q, const void* k_cache, const void* v_cache, const int32_t* seqlens_k,
+                                const int32_t* page_table, int max_blocks_per_seq, int num_blocks, int cache_capacity,
+                                int max_seqlen_k, void* o, int o_dtype, float* lse, int B, int T, int Hq, int Hkv,
+                                int d, float scale, int window, int sinks, int num_splits, void* workspace,
+                                size_t workspace_bytes, void* stream);
+ATTN_API int attn_decode_window_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                    const float* v_scale, const int32_t* seqlens_k, const int32_t* page_table,
+                                    int max_blocks_per_seq, int num_blocks, int cache_capacity, int max_seqlen_k,
+                                    void* o, int o_dtype, float* lse, int B, int T, int Hq, int Hkv, int d,
+                                    float scale, int window, int sinks, int num_splits, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of attn_decode_shared and attn_decode_shared_fp8; 0 for invalid sizes.
+ * prefix_blocks = 0 gives attn_decode_workspace_bytes. */
+ATTN_API size_t attn_decode_shared_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int max_seqlen_k,
+                                                   int prefix_blocks, int num_splits);
+
+/*
+ * attn_decode_shared, attn_decode_shared_fp8 -- decode of a batch whose sequences
+ * share their first prefix_blocks blocks (forks of one prompt, requests behind one
+ * system prompt; [P1] "页面注意 KV缓存作为虚拟内存": blocks shared between parallel
+ * samples).  The prefix's K and V are read once for the whole batch: the queries of
+ * all sequences meet them as one tile of rows, each sequence's queries then meet
+ * its own keys, and the two parts are merged by their log-sum-exps ([P3] "背景", the
+ * stable reduction of partial softmax results).  Same result as attn_decode over
+ * tables whose first prefix_blocks entries are prefix_table's.
+ *
+ *   k_cache, v_cache  paged pools [num_blocks, 16, Hkv, d] (sharing needs pages)
+ *   page_table        device int32 [B, max_blocks_per_seq], required; the first
+ *                     prefix_blocks entries of its rows are NOT read
+ *   prefix_table      device int32 [prefix_blocks]: the shared blocks, in order (row
+ *                     0 of page_table serves); may be NULL when prefix_blocks is 0,
+ *                     which is attn_decode / attn_decode_fp8
+ *   seqlens_k         keys of sequence b INCLUDING the prefix and the T new tokens:
+ *                     at least 16 * prefix_blocks + T
+ *   num_splits        0 = automatic; n > 0 = the prefix and each own part in at
+ *                     most n chunks each
+ *   everything else   as for attn_decode / attn_decode_fp8, with
+ *                     attn_decode_shared_workspace_bytes for the workspace
+ * Errors: attn_decode's; ATTN_ERR_INVALID_ARG when prefix_blocks exceeds
+ * max_blocks_per_seq or 16 * prefix_blocks + T exceeds max_seqlen_k;
+ * ATTN_ERR_UNSUPPORTED for B * T above 2^24 - 1.  A length below
+ * 16 * prefix_blocks + T sets ATTN_DEV_SEQLEN and makes that sequence's rows NaN.
+ */
+ATTN_API int attn_decode_shared(const void* q, const void* k_cache, const void* v_cache, const int32_t* seqlens_k,
+                                const int32_t* page_table, int max_blocks_per_seq, int num_blocks,
+                                const int32_t* prefix_table, int prefix_blocks, int max_seqlen_k, void* o, int o_dtype,
+                                float* lse, int B, int T, int Hq, int Hkv, int d, float scale, int causal,
+                                int num_splits, void* workspace, size_t workspace_bytes, void* stream);
+ATTN_API int attn_decode_shared_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                    const float* v_scale, const int32_t* seqlens_k, const int32_t* page_table,
+                                    int max_blocks_per_seq, int num_blocks, const int32_t* prefix_table,
+                                    int prefix_blocks, int max_seqlen_k, void* o, int o_dtype, float* lse, int B,
+                                    int T, int Hq, int Hkv, int d, float scale, int causal, int num_splits,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * rope_table_fill -- angle table of the rotary position embedding: row p holds
+ * cos(p * theta^(-2i / rot_dim)) for i < rot_dim / 2, then the sines; angles in 64
+ * bits, each value rounded once to fp32.  A table with other angles (scaled or
+ * extended positions) in the same layout serves the calls below as well.
+ *   table  device fp32 [rows, rot_dim];  rows >= 1, rot_dim even >= 2, theta > 0
+ */
+ATTN_API int rope_table_fill(float* table, int rows, int rot_dim, double theta, void* stream);
+
+/*
+ * qk_norm_rope -- per-head RMS norm of queries and keys and the rotary position
+ * embedding, in one pass over a prompt's q and k.  The pages start after this step
+ * (their q and k are the projections'); it is what a model with normalised heads
+ * runs between its projection and attn_prefill.
+ *
+ * For each head's row x of the token at position p = pos0[b] + t:
+ *   y_i = x_i * rsqrt(mean_j x_j^2 + eps) * weight_i       (weight NULL: y = x)
+ *   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)
+ * for the rot_dim / 2 pairs (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) with
+ * interleaved = 1; elements from rot_dim on are not rotated.  fp32 arithmetic,
+ * rounded once.
+ *
+ *   q, k         device bf16, the rows of B * T tokens: Hq (Hkv) * d contiguous
+ *                values every q_stride (k_stride) elements, so views of a fused
+ *                projection output work; strides are multiples of 8, >= Hq (Hkv) * d
+ *   q_out, k_out device bf16 [B, T, Hq, d] and [B, T, Hkv, d], contiguous; each may be
+ *                its own input when that is contiguous, and overlap nothing else
+ *   q_weight, k_weight  device bf16 [d], or NULL
+ *   eps          > 0, finite (ignored when both weights are NULL)
+ *   rope         device fp32 [rope_rows, rot_dim] (rope_table_fill), or NULL with
+ *                rot_dim = 0: no rotation
+ *   pos0         device int32 [B], or NULL for 0
+ *   d            64 or 128;  rot_dim a multiple of 16, <= d
+ * All pointers 16-byte aligned.  Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED
+ * (d, rot_dim not a multiple of 16, B * T above 2^31 - 1), ATTN_ERR_CUDA.  A
+ * position outside the table makes that token's rows NaN and sets ATTN_DEV_POSITION.
+ */
+ATTN_API int qk_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride, void* q_out, void* k_out,
+                          const void* q_weight, const void* k_weight, float eps, const float* rope, int rope_rows,
+                          int rot_dim, int interleaved, const int32_t* pos0, int B, int T, int Hq, int Hkv, int d,
+                          void* stream);
+
+/*
+ * kv_append_norm_rope, kv_append_norm_rope_fp8 -- qk_norm_rope and kv_append /
+ * kv_append_fp8 in one pass: the new tokens' queries are normalised and rotated
+ * into q_out, their keys normalised, rotated and written to the cache at positions
+ * cache_lens[b] + t (which are also the angles' positions), their values written
+ * beside them unchanged.  The FP8 form quantises the fp32 result as kv_append_fp8
+ * quantises its bf16 input (one rounding: k is not rounded to bf16 in between).
+ *
+ *   k_cache, v_cache, cache_lens, page_table, ...  as for kv_append / kv_append_fp8
+ *   q, k_new, v_new   token rows with strides, as q and k of qk_norm_rope
+ *   everything else   as for qk_norm_rope
+ * A position outside the angle table leaves the cache as it was, makes that token's
+ * q_out rows NaN and sets ATTN_DEV_POSITION; positions beyond the cache, bad page
+ * ids and bad scales are kv_append's (q_out is then still written).
+ */
+ATTN_API int kv_append_norm_rope(void* k_cache, void* v_cache, const void* q, const void* k_new, const void* v_new,
+                                 int64_t q_stride, int64_t k_stride, int64_t v_stride, void* q_out,
+                                 const void* q_weight, const void* k_weight, float eps, const float* rope,
+                                 int rope_rows, int rot_dim, int interleaved, const int32_t* cache_lens,
+                                 const int32_t* page_table, int max_blocks_per_seq, int num_blocks,
+                                 int cache_capacity, int B, int T, int Hq, int Hkv, int d, void* stream);
+ATTN_API int kv_append_norm_rope_fp8(void* k_cache, void* v_cache, const void* q, const void* k_new,
+                                     const void* v_new, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                     void* q_out, const float* k_scale, const float* v_scale, const void* q_weight,
+                                     const void* k_weight, float eps, const float* rope, int rope_rows, int rot_dim,
+                                     int interleaved, const int32_t* cache_lens, const int32_t* page_table,
+                                     int max_blocks_per_seq, int num_blocks, int cache_capacity, int B, int T, int Hq,
+                                     int Hkv, int d, void* stream);
 
 /*
  * kv_cache_bytes -- bytes held by a KV cache: 2 * n_layers * batch * tokens *

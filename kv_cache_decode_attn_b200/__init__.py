@@ -22,12 +22,17 @@ __all__ = [
     "lib", "LIB_PATH", "AttnError",
     "attn_prefill", "attn_decode", "attn_decode_workspace_bytes", "attn_decode_noalloc", "kv_append",
     "attn_decode_fp8", "kv_append_fp8", "attn_prefill_cache", "BlockPool", "copy_blocks", "pool_simulate",
+    "attn_prefill_window", "attn_prefill_cache_window", "attn_decode_window", "attn_decode_window_fp8",
+    "attn_decode_window_workspace_bytes", "decode_window_workspace",
+    "attn_decode_shared", "attn_decode_shared_fp8", "attn_decode_shared_workspace_bytes", "decode_shared_workspace",
+    "qk_norm_rope", "kv_append_norm_rope", "kv_append_norm_rope_fp8", "rope_table_fill", "rope_table",
     "ATTN_ERR_NO_BLOCKS", "SIM_METRICS",
     "kv_cache_bytes", "ATTN_DECODE_NOALLOC_SCRATCH_BYTES",
     "attn_get_device_status", "attn_selftest_wait_timeout", "attn_status_string", "decode_workspace",
     "ATTN_OK", "ATTN_ERR_INVALID_ARG", "ATTN_ERR_UNSUPPORTED", "ATTN_ERR_WORKSPACE", "ATTN_ERR_CUDA",
     "ATTN_ERR_DEVICE", "ATTN_F32", "ATTN_BF16", "ATTN_DEV_PAGE_ID", "ATTN_DEV_SEQLEN",
     "ATTN_DEV_APPEND_RANGE", "ATTN_DEV_TIMEOUT", "ATTN_DEV_SCALE",
+    "ATTN_DEV_POSITION",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkvattn.so")
@@ -41,8 +46,10 @@ SIM_METRICS = ["paged_rejected", "paged_dropped", "paged_peak_reserved", "paged_
 ATTN_F32, ATTN_BF16 = 0, 1
 ATTN_DECODE_NOALLOC_SCRATCH_BYTES = 32 << 20
 ATTN_DEV_PAGE_ID, ATTN_DEV_SEQLEN, ATTN_DEV_APPEND_RANGE, ATTN_DEV_TIMEOUT, ATTN_DEV_SCALE = 1, 2, 4, 8, 16
+ATTN_DEV_POSITION = 32
 
 _p, _i, _i64, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+_d = ctypes.c_double
 
 _SIGNATURES = {
     "attn_prefill": (_i, [_p, _p, _p, _p, _i, _p, _i, _i, _i, _i, _i, _f, _i, _p]),
@@ -56,6 +63,25 @@ _SIGNATURES = {
                              _i, _p, _sz, _p]),
     "kv_append": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _p]),
     "kv_append_fp8": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _p]),
+    "attn_prefill_window": (_i, [_p, _p, _p, _p, _i, _p, _i, _i, _i, _i, _i, _f, _i, _i, _p]),
+    "attn_prefill_cache_window": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _p, _i, _p, _i, _i, _i, _i, _i, _f, _i, _i,
+                                       _p]),
+    "attn_decode_window_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i]),
+    "attn_decode_window": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _i, _p, _i, _i, _i, _i, _i, _f, _i, _i, _i,
+                                _p, _sz, _p]),
+    "attn_decode_window_fp8": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _i, _p, _i, _i, _i, _i, _i, _f,
+                                    _i, _i, _i, _p, _sz, _p]),
+    "attn_decode_shared_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
+    "attn_decode_shared": (_i, [_p, _p, _p, _p, _p, _i, _i, _p, _i, _i, _p, _i, _p, _i, _i, _i, _i, _i, _f, _i, _i,
+                                _p, _sz, _p]),
+    "attn_decode_shared_fp8": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _p, _i, _i, _p, _i, _p, _i, _i, _i, _i, _i,
+                                    _f, _i, _i, _p, _sz, _p]),
+    "rope_table_fill": (_i, [_p, _i, _i, _d, _p]),
+    "qk_norm_rope": (_i, [_p, _p, _i64, _i64, _p, _p, _p, _p, _f, _p, _i, _i, _i, _p, _i, _i, _i, _i, _i, _p]),
+    "kv_append_norm_rope": (_i, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _p, _f, _p, _i, _i, _i, _p, _p, _i, _i,
+                                 _i, _i, _i, _i, _i, _i, _p]),
+    "kv_append_norm_rope_fp8": (_i, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p, _f, _p, _i, _i, _i, _p,
+                                     _p, _i, _i, _i, _i, _i, _i, _i, _i, _p]),
     "kv_cache_bytes": (_i64, [_i, _i, _i64, _i, _i, _i]),
     "attn_block_pool_create": (_p, [_i, _i]),
     "attn_block_pool_destroy": (None, [_p]),
@@ -127,6 +153,42 @@ def _out_dtype(o: torch.Tensor) -> int:
     if o.dtype == torch.bfloat16:
         return ATTN_BF16
     raise ValueError("output must be float32 or bfloat16")
+
+
+def _int32(n) -> int:
+    """A window, sink count or the like as the C int it is passed as."""
+    n = int(n)
+    if not -2**31 <= n < 2**31:
+        raise ValueError("value does not fit in 32 bits")
+    return n
+
+
+def _on_current_device(*tensors) -> None:
+    """The calls run on the current device: every tensor has to be on it."""
+    used = {t.device for t in tensors if t is not None and t.is_cuda}
+    if used and used != {torch.device("cuda", torch.cuda.current_device())}:
+        raise ValueError(f"tensors on {sorted(map(str, used))}, the current device is {torch.cuda.current_device()}")
+
+
+def _cache_fits(k_cache, page_table, lens, B, d) -> None:
+    """The cache, page table and lengths belong to B sequences of head size d."""
+    if int(k_cache.shape[3]) != d or tuple(lens.shape) != (B,):
+        raise ValueError("shape mismatch")
+    if page_table is None:
+        if int(k_cache.shape[0]) != B:
+            raise ValueError("a contiguous cache must be [B, capacity, Hkv, d]")
+    elif int(k_cache.shape[1]) != 16 or int(page_table.shape[0]) != B:
+        raise ValueError("a paged cache must be [num_blocks, 16, Hkv, d] with a page table [B, max_blocks]")
+
+
+def _caches(k_cache, v_cache, scales, Hkv):
+    """Pointers of a bf16 cache (scales None) or of an FP8 cache and its scales."""
+    if scales is None:
+        return (_dev(k_cache, "k_cache", torch.bfloat16), _dev(v_cache, "v_cache", torch.bfloat16)), ()
+    if any(tuple(s.shape) != (Hkv,) for s in scales):
+        raise ValueError("k_scale and v_scale must be [Hkv]")
+    return ((_codes(k_cache, "k_cache"), _codes(v_cache, "v_cache")),
+            (_dev(scales[0], "k_scale", torch.float32), _dev(scales[1], "v_scale", torch.float32)))
 
 
 def attn_prefill(q, k, v, o, lse=None, scale=None, causal=True, stream=None) -> None:
@@ -297,6 +359,268 @@ def kv_append_fp8(k_cache, v_cache, k_new, v_new, k_scale, v_scale, cache_lens, 
                            None if page_table is None else _dev(page_table, "page_table", torch.int32),
                            max_blocks, num_blocks, cap, B, T, Hkv, d, _stream(stream))
     _check("kv_append_fp8", st)
+
+
+# ------------------------------------------- sliding window with first tokens visible
+def attn_prefill_window(q, k, v, o, window, sinks=0, lse=None, scale=None, stream=None) -> None:
+    """``attn_prefill`` (causal) where the query at position p sees keys j <= p with
+    j > p - window or j < sinks."""
+    B, N, Hq, d = q.shape
+    Hkv = k.shape[2]
+    if tuple(k.shape) != (B, N, Hkv, d) or tuple(v.shape) != tuple(k.shape) or tuple(o.shape) != (B, N, Hq, d):
+        raise ValueError("shape mismatch")
+    if lse is not None and tuple(lse.shape) != (B, Hq, N):
+        raise ValueError("lse must be [B, Hq, N]")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    _on_current_device(q, k, v, o, lse)
+    st = lib.attn_prefill_window(_dev(q, "q", torch.bfloat16), _dev(k, "k", torch.bfloat16),
+                                 _dev(v, "v", torch.bfloat16), _dev(o, "o"), _out_dtype(o),
+                                 None if lse is None else _dev(lse, "lse", torch.float32), B, Hq, Hkv, N, d, scale,
+                                 _int32(window), _int32(sinks), _stream(stream))
+    _check("attn_prefill_window", st)
+
+
+def attn_prefill_cache_window(q, k_cache, v_cache, seqlens_k, o, window, sinks=0, lse=None, page_table=None,
+                              scale=None, stream=None) -> None:
+    """``attn_prefill_cache`` (causal) with the mask of ``attn_prefill_window``; positions count
+    from the start of the cached sequence."""
+    B, Nq, Hq, d = q.shape
+    max_blocks, num_blocks, cap, Hkv = _cache_geometry(k_cache, page_table)
+    if tuple(v_cache.shape) != tuple(k_cache.shape) or tuple(o.shape) != (B, Nq, Hq, d):
+        raise ValueError("shape mismatch")
+    _cache_fits(k_cache, page_table, seqlens_k, B, d)
+    if lse is not None and tuple(lse.shape) != (B, Hq, Nq):
+        raise ValueError("lse must be [B, Hq, Nq]")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    _on_current_device(q, k_cache, v_cache, seqlens_k, o, lse, page_table)
+    st = lib.attn_prefill_cache_window(
+        _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache", torch.bfloat16),
+        _dev(v_cache, "v_cache", torch.bfloat16), _dev(seqlens_k, "seqlens_k", torch.int32),
+        None if page_table is None else _dev(page_table, "page_table", torch.int32), max_blocks, num_blocks, cap,
+        _dev(o, "o"), _out_dtype(o), None if lse is None else _dev(lse, "lse", torch.float32), B, Nq, Hq, Hkv, d,
+        scale, _int32(window), _int32(sinks), _stream(stream))
+    _check("attn_prefill_cache_window", st)
+
+
+def attn_decode_window_workspace_bytes(B, T, Hq, Hkv, d, max_seqlen_k, window, sinks=0, num_splits=0) -> int:
+    return int(lib.attn_decode_window_workspace_bytes(B, T, Hq, Hkv, d, max_seqlen_k, _int32(window), _int32(sinks),
+                                                      num_splits))
+
+
+def decode_window_workspace(B, T, Hq, Hkv, d, max_seqlen_k, window, sinks=0, num_splits=0,
+                            device="cuda") -> torch.Tensor:
+    """Caller-owned workspace for ``attn_decode_window`` and its FP8 form (allocated by torch)."""
+    n = attn_decode_window_workspace_bytes(B, T, Hq, Hkv, d, max_seqlen_k, window, sinks, num_splits)
+    if n == 0:
+        raise ValueError("invalid decode sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _decode_window(name, q, k_cache, v_cache, scales, seqlens_k, o, window, sinks, lse, page_table, max_seqlen_k, scale,
+                   num_splits, workspace, stream) -> None:
+    B, T, Hq, d = q.shape
+    max_blocks, num_blocks, cap, Hkv = _cache_geometry(k_cache, page_table)
+    if tuple(v_cache.shape) != tuple(k_cache.shape) or tuple(o.shape) != (B, T, Hq, d):
+        raise ValueError("shape mismatch")
+    _cache_fits(k_cache, page_table, seqlens_k, B, d)
+    if lse is not None and tuple(lse.shape) != (B, Hq, T):
+        raise ValueError("lse must be [B, Hq, T]")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    if workspace is None:
+        msk = max_seqlen_k if max_seqlen_k else (cap if page_table is None else max_blocks * 16)
+        workspace = decode_window_workspace(B, T, Hq, Hkv, d, msk, window, sinks, num_splits, q.device)
+    _on_current_device(q, k_cache, v_cache, *(scales or ()), seqlens_k, o, lse, page_table, workspace)
+    caches, more = _caches(k_cache, v_cache, scales, Hkv)
+    st = getattr(lib, name)(_dev(q, "q", torch.bfloat16), *caches, *more, _dev(seqlens_k, "seqlens_k", torch.int32),
+                            None if page_table is None else _dev(page_table, "page_table", torch.int32),
+                            max_blocks, num_blocks, cap, int(max_seqlen_k), _dev(o, "o"), _out_dtype(o),
+                            None if lse is None else _dev(lse, "lse", torch.float32), B, T, Hq, Hkv, d, scale,
+                            _int32(window), _int32(sinks), int(num_splits), _dev(workspace, "workspace"),
+                            workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(name, st)
+
+
+def attn_decode_window(q, k_cache, v_cache, seqlens_k, o, window, sinks=0, lse=None, page_table=None, max_seqlen_k=0,
+                       scale=None, num_splits=0, workspace=None, stream=None) -> None:
+    """``attn_decode`` (causal) where token t, at position p = seqlens_k[b] - T + t, sees keys
+    j <= p with j > p - window or j < sinks.  Only the blocks holding such keys are read."""
+    _decode_window("attn_decode_window", q, k_cache, v_cache, None, seqlens_k, o, window, sinks, lse, page_table,
+                   max_seqlen_k, scale, num_splits, workspace, stream)
+
+
+def attn_decode_window_fp8(q, k_cache, v_cache, k_scale, v_scale, seqlens_k, o, window, sinks=0, lse=None,
+                           page_table=None, max_seqlen_k=0, scale=None, num_splits=0, workspace=None,
+                           stream=None) -> None:
+    """``attn_decode_window`` over an FP8 cache (arguments as ``attn_decode_fp8``)."""
+    _decode_window("attn_decode_window_fp8", q, k_cache, v_cache, (k_scale, v_scale), seqlens_k, o, window, sinks, lse,
+                   page_table, max_seqlen_k, scale, num_splits, workspace, stream)
+
+
+# ------------------------------------------------------------------ shared prefix
+def attn_decode_shared_workspace_bytes(B, T, Hq, Hkv, d, max_seqlen_k, prefix_blocks, num_splits=0) -> int:
+    return int(lib.attn_decode_shared_workspace_bytes(B, T, Hq, Hkv, d, max_seqlen_k, prefix_blocks, num_splits))
+
+
+def decode_shared_workspace(B, T, Hq, Hkv, d, max_seqlen_k, prefix_blocks, num_splits=0,
+                            device="cuda") -> torch.Tensor:
+    """Caller-owned workspace for ``attn_decode_shared`` and its FP8 form (allocated by torch)."""
+    n = attn_decode_shared_workspace_bytes(B, T, Hq, Hkv, d, max_seqlen_k, prefix_blocks, num_splits)
+    if n == 0:
+        raise ValueError("invalid decode sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _decode_shared(name, q, k_cache, v_cache, scales, seqlens_k, page_table, prefix_table, o, lse, max_seqlen_k, scale,
+                   causal, num_splits, workspace, stream) -> None:
+    B, T, Hq, d = q.shape
+    max_blocks, num_blocks, _, Hkv = _cache_geometry(k_cache, page_table)
+    if tuple(v_cache.shape) != tuple(k_cache.shape) or tuple(o.shape) != (B, T, Hq, d):
+        raise ValueError("shape mismatch")
+    _cache_fits(k_cache, page_table, seqlens_k, B, d)
+    if prefix_table.dim() != 1:
+        raise ValueError("prefix_table must be [prefix_blocks]")
+    if lse is not None and tuple(lse.shape) != (B, Hq, T):
+        raise ValueError("lse must be [B, Hq, T]")
+    n = int(prefix_table.shape[0])
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    if workspace is None:
+        msk = max_seqlen_k if max_seqlen_k else max_blocks * 16
+        workspace = decode_shared_workspace(B, T, Hq, Hkv, d, msk, n, num_splits, q.device)
+    _on_current_device(q, k_cache, v_cache, *(scales or ()), seqlens_k, o, lse, page_table, prefix_table, workspace)
+    caches, more = _caches(k_cache, v_cache, scales, Hkv)
+    st = getattr(lib, name)(_dev(q, "q", torch.bfloat16), *caches, *more, _dev(seqlens_k, "seqlens_k", torch.int32),
+                            _dev(page_table, "page_table", torch.int32), max_blocks, num_blocks,
+                            _dev(prefix_table, "prefix_table", torch.int32) if n else None, n, int(max_seqlen_k),
+                            _dev(o, "o"), _out_dtype(o), None if lse is None else _dev(lse, "lse", torch.float32),
+                            B, T, Hq, Hkv, d, scale, int(bool(causal)), int(num_splits), _dev(workspace, "workspace"),
+                            workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(name, st)
+
+
+def attn_decode_shared(q, k_cache, v_cache, seqlens_k, page_table, prefix_table, o, lse=None, max_seqlen_k=0,
+                       scale=None, causal=True, num_splits=0, workspace=None, stream=None) -> None:
+    """``attn_decode`` over pools ``[nblk, 16, Hkv, d]`` for a batch whose sequences share their
+    first blocks: prefix_table int32 ``[prefix_blocks]`` names them (``page_table[0, :n]`` serves)
+    and page_table's first prefix_blocks columns are not read.  The prefix is read once for the
+    whole batch.  seqlens_k counts the prefix and the T new tokens."""
+    _decode_shared("attn_decode_shared", q, k_cache, v_cache, None, seqlens_k, page_table, prefix_table, o, lse,
+                   max_seqlen_k, scale, causal, num_splits, workspace, stream)
+
+
+def attn_decode_shared_fp8(q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_table, prefix_table, o, lse=None,
+                           max_seqlen_k=0, scale=None, causal=True, num_splits=0, workspace=None,
+                           stream=None) -> None:
+    """``attn_decode_shared`` over an FP8 cache (scales as ``attn_decode_fp8``)."""
+    _decode_shared("attn_decode_shared_fp8", q, k_cache, v_cache, (k_scale, v_scale), seqlens_k, page_table,
+                   prefix_table, o, lse, max_seqlen_k, scale, causal, num_splits, workspace, stream)
+
+
+# ------------------------------------------------- norm, rotation and append in one pass
+def rope_table_fill(table, theta=10000.0, stream=None) -> None:
+    """Fill ``table`` fp32 ``[rows, rot_dim]``: row p holds the cosines of p * theta^(-2i / rot_dim),
+    then the sines (angles in 64 bits)."""
+    if table.dim() != 2:
+        raise ValueError("table must be [rows, rot_dim]")
+    _on_current_device(table)
+    _check("rope_table_fill", lib.rope_table_fill(_dev(table, "table", torch.float32), int(table.shape[0]),
+                                                  int(table.shape[1]), float(theta), _stream(stream)))
+
+
+def rope_table(rows, rot_dim, theta=10000.0, device="cuda", stream=None) -> torch.Tensor:
+    """A new angle table for positions 0 .. rows - 1 (``rope_table_fill``)."""
+    table = torch.empty(int(rows), int(rot_dim), dtype=torch.float32, device=device)
+    rope_table_fill(table, theta, stream)
+    return table
+
+
+def _token_rows(t, name):
+    """Pointer and token stride (elements) of a bf16 ``[B, T, H, d]`` tensor whose tokens' rows are
+    contiguous and evenly spaced over B * T: contiguous, or a view of a fused projection output."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}")
+    B, T, H, d = t.shape
+    sb, st, sh, sd = t.stride()
+    step = st if T > 1 else (sb if B > 1 else H * d)
+    if (d > 1 and sd != 1) or (H > 1 and sh != d) or (B > 1 and T > 1 and sb != T * st):
+        raise ValueError(f"{name}: each token's heads must be contiguous and the tokens evenly spaced")
+    return t.data_ptr(), step
+
+
+def _norm_rope_args(q, k, q_weight, k_weight, rope, d):
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and tuple(w.shape) != (d,):
+            raise ValueError(f"{n} must be [d]")
+    if rope is not None and rope.dim() != 2:
+        raise ValueError("rope must be [rows, rot_dim]")
+    return (None if q_weight is None else _dev(q_weight, "q_weight", torch.bfloat16),
+            None if k_weight is None else _dev(k_weight, "k_weight", torch.bfloat16),
+            None if rope is None else _dev(rope, "rope", torch.float32),
+            0 if rope is None else int(rope.shape[0]), 0 if rope is None else int(rope.shape[1]))
+
+
+def qk_norm_rope(q, k, q_out, k_out, rope, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, pos0=None,
+                 stream=None) -> None:
+    """Per-head RMS norm (with a weight ``[d]``) and rotation of q ``[B, T, Hq, d]`` and k
+    ``[B, T, Hkv, d]`` bf16, which may be views of a fused projection output, into contiguous q_out
+    and k_out.  rope fp32 ``[rows, rot_dim]`` (``rope_table``) or None; pos0 int32 ``[B]`` is the
+    position of each sequence's token 0 (default 0)."""
+    B, T, Hq, d = q.shape
+    Hkv = k.shape[2]
+    if tuple(k.shape) != (B, T, Hkv, d) or tuple(q_out.shape) != (B, T, Hq, d) or tuple(k_out.shape) != tuple(k.shape):
+        raise ValueError("shape mismatch")
+    if pos0 is not None and tuple(pos0.shape) != (B,):
+        raise ValueError("pos0 must be [B]")
+    qp, qs = _token_rows(q, "q")
+    kp, ks = _token_rows(k, "k")
+    qw, kw, tab, rows, rot = _norm_rope_args(q, k, q_weight, k_weight, rope, d)
+    _on_current_device(q, k, q_out, k_out, rope, q_weight, k_weight, pos0)
+    st = lib.qk_norm_rope(qp, kp, qs, ks, _dev(q_out, "q_out", torch.bfloat16), _dev(k_out, "k_out", torch.bfloat16),
+                          qw, kw, float(eps), tab, rows, rot, int(bool(interleaved)),
+                          None if pos0 is None else _dev(pos0, "pos0", torch.int32), B, T, Hq, Hkv, d,
+                          _stream(stream))
+    _check("qk_norm_rope", st)
+
+
+def _append_norm_rope(name, k_cache, v_cache, q, k_new, v_new, q_out, scales, rope, cache_lens, page_table, q_weight,
+                      k_weight, eps, interleaved, stream) -> None:
+    B, T, Hq, d = q.shape
+    Hkv = k_new.shape[2]
+    max_blocks, num_blocks, cap, Hkv_c = _cache_geometry(k_cache, page_table)
+    if tuple(k_new.shape) != (B, T, Hkv, d) or tuple(v_new.shape) != tuple(k_new.shape) or Hkv_c != Hkv \
+            or tuple(q_out.shape) != (B, T, Hq, d) or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("shape mismatch")
+    _cache_fits(k_cache, page_table, cache_lens, B, d)
+    qp, qs = _token_rows(q, "q")
+    kp, ks = _token_rows(k_new, "k_new")
+    vp, vs = _token_rows(v_new, "v_new")
+    qw, kw, tab, rows, rot = _norm_rope_args(q, k_new, q_weight, k_weight, rope, d)
+    caches, more = _caches(k_cache, v_cache, scales, Hkv)
+    _on_current_device(k_cache, v_cache, q, k_new, v_new, q_out, *(scales or ()), rope, cache_lens, page_table, q_weight,
+                       k_weight)
+    st = getattr(lib, name)(*caches, qp, kp, vp, qs, ks, vs, _dev(q_out, "q_out", torch.bfloat16), *more, qw, kw,
+                            float(eps), tab, rows, rot, int(bool(interleaved)),
+                            _dev(cache_lens, "cache_lens", torch.int32),
+                            None if page_table is None else _dev(page_table, "page_table", torch.int32),
+                            max_blocks, num_blocks, cap, B, T, Hq, Hkv, d, _stream(stream))
+    _check(name, st)
+
+
+def kv_append_norm_rope(k_cache, v_cache, q, k_new, v_new, q_out, rope, cache_lens, page_table=None, q_weight=None,
+                        k_weight=None, eps=1e-6, interleaved=False, stream=None) -> None:
+    """``qk_norm_rope`` of the new tokens at positions cache_lens[b] + t, with the keys and values
+    written to the cache (as ``kv_append``) and the queries to q_out ``[B, T, Hq, d]``."""
+    _append_norm_rope("kv_append_norm_rope", k_cache, v_cache, q, k_new, v_new, q_out, None, rope, cache_lens,
+                      page_table, q_weight, k_weight, eps, interleaved, stream)
+
+
+def kv_append_norm_rope_fp8(k_cache, v_cache, q, k_new, v_new, q_out, k_scale, v_scale, rope, cache_lens,
+                            page_table=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                            stream=None) -> None:
+    """``kv_append_norm_rope`` into an FP8 cache (quantised as ``kv_append_fp8`` does)."""
+    _append_norm_rope("kv_append_norm_rope_fp8", k_cache, v_cache, q, k_new, v_new, q_out, (k_scale, v_scale), rope,
+                      cache_lens, page_table, q_weight, k_weight, eps, interleaved, stream)
 
 
 def kv_cache_bytes(n_layers, batch, tokens, n_kv_heads, head_dim, elem_bytes) -> int:

@@ -6,6 +6,7 @@
 #include <stdio.h>
 #include <stdlib.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "../../include/attn.h"
@@ -79,6 +80,13 @@ using namespace kvattn;
 
 namespace {
 
+// Longest selected range of a windowed decode: the first tokens' blocks, and the keys
+// from the first query's window on, rounded down to a whole block.
+int window_max_keys(int max_seqlen_k, int T, int window, int sinks) {
+  const long long s16 = ((long long)sinks + kPageTokens - 1) / kPageTokens * kPageTokens;
+  return (int)std::min<long long>(max_seqlen_k, s16 + window + T - 1 + kPageTokens - 1);
+}
+
 struct DecodeLayout {
   int R, chunk, max_chunks;
   int balanced, n_chunks;   // balanced split: chunks over the batch (per KV head)
@@ -117,6 +125,42 @@ int cuda_status(cudaError_t e, const char* where) {
   static const bool debug = getenv("KVATTN_DEBUG") != nullptr;
   if (debug) fprintf(stderr, "[kvattn] %s: %s (%d)\n", where, cudaGetErrorString(e), (int)e);
   return ATTN_ERR_CUDA;
+}
+
+int prefill_impl(const void* q, const void* k, const void* v, void* o, int o_dtype, float* lse, int B, int Hq,
+                 int Hkv, int N, int d, float scale, int causal, bool windowed, int window, int sinks, void* stream,
+                 const char* name) {
+  if (!q || !k || !v || !o) return ATTN_ERR_INVALID_ARG;
+  if (B < 1 || Hq < 1 || Hkv < 1 || N < 1 || Hq % Hkv) return ATTN_ERR_INVALID_ARG;
+  if (o_dtype != ATTN_F32 && o_dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !isfinite(scale) || (causal != 0 && causal != 1)) return ATTN_ERR_INVALID_ARG;
+  if (windowed && (window < 1 || sinks < 0)) return ATTN_ERR_INVALID_ARG;
+  if (windowed && N > kMaxDecodeSeqlen) return ATTN_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
+  if ((long long)B * N * Hq > INT32_MAX || (long long)B * N * Hkv > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+  unsigned* st = status_ptr();
+  if (!st) return ATTN_ERR_CUDA;
+  PrefillLaunch a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.o_bf16 = o_dtype == ATTN_BF16;
+  a.lse = lse;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.N = N;
+  a.d = d;
+  a.scale = scale;
+  a.causal = causal;
+  a.status = st;
+  if (windowed) {   // the same keys, and no overflow
+    a.window = std::min(window, N);
+    a.sinks = std::min(sinks, N);
+  }
+  return cuda_status(launch_prefill(a, static_cast<cudaStream_t>(stream)), name);
 }
 
 }  // namespace
@@ -170,31 +214,7 @@ size_t attn_decode_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int max
 
 int attn_prefill(const void* q, const void* k, const void* v, void* o, int o_dtype, float* lse, int B, int Hq,
                  int Hkv, int N, int d, float scale, int causal, void* stream) {
-  if (!q || !k || !v || !o) return ATTN_ERR_INVALID_ARG;
-  if (B < 1 || Hq < 1 || Hkv < 1 || N < 1 || Hq % Hkv) return ATTN_ERR_INVALID_ARG;
-  if (o_dtype != ATTN_F32 && o_dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !isfinite(scale) || (causal != 0 && causal != 1)) return ATTN_ERR_INVALID_ARG;
-  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
-  if ((long long)B * N * Hq > INT32_MAX || (long long)B * N * Hkv > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
-  unsigned* st = status_ptr();
-  if (!st) return ATTN_ERR_CUDA;
-  PrefillLaunch a;
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.o = o;
-  a.o_bf16 = o_dtype == ATTN_BF16;
-  a.lse = lse;
-  a.B = B;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.N = N;
-  a.d = d;
-  a.scale = scale;
-  a.causal = causal;
-  a.status = st;
-  return cuda_status(launch_prefill(a, static_cast<cudaStream_t>(stream)), "attn_prefill");
+  return prefill_impl(q, k, v, o, o_dtype, lse, B, Hq, Hkv, N, d, scale, causal, false, 0, 0, stream, "attn_prefill");
 }
 
 }  // extern "C"
@@ -205,7 +225,8 @@ int decode_impl(const void* q, const void* k_cache, const void* v_cache, const f
                 bool fp8, const int32_t* seqlens_k, const int32_t* page_table, int max_blocks_per_seq,
                 int num_blocks, int cache_capacity, int max_seqlen_k, void* o, int o_dtype, float* lse, int B, int T,
                 int Hq, int Hkv, int d, float scale, int causal, int num_splits, void* workspace,
-                size_t workspace_bytes, void* stream, const char* name, bool static_scratch = false) {
+                size_t workspace_bytes, void* stream, const char* name, bool static_scratch = false,
+                int window = 0, int sinks = 0) {
   if (!q || !k_cache || !v_cache || !seqlens_k || !o) return ATTN_ERR_INVALID_ARG;
   if (fp8 && (!k_scale || !v_scale)) return ATTN_ERR_INVALID_ARG;
   if (B < 1 || T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || num_splits < 0) return ATTN_ERR_INVALID_ARG;
@@ -229,8 +250,9 @@ int decode_impl(const void* q, const void* k_cache, const void* v_cache, const f
   if (Hq / Hkv > 128) return ATTN_ERR_UNSUPPORTED;                       // one token's heads must fit a row tile
   if (fp8 && d != 128) return ATTN_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
+  const int max_keys = window > 0 ? window_max_keys(max_seqlen_k, T, window, sinks) : max_seqlen_k;
   DecodeLayout L;
-  if (!decode_layout(B, T, Hq, Hkv, d, max_seqlen_k, num_splits, fp8, &L)) return ATTN_ERR_INVALID_ARG;
+  if (!decode_layout(B, T, Hq, Hkv, d, max_keys, num_splits, fp8, &L)) return ATTN_ERR_INVALID_ARG;
   if (workspace_bytes < L.total) return ATTN_ERR_WORKSPACE;
   if (static_scratch) {
     // attn_decode_noalloc: the library's own array, looked up only once the request is known to be valid
@@ -265,6 +287,8 @@ int decode_impl(const void* q, const void* k_cache, const void* v_cache, const f
     pa.max_blocks = max_blocks_per_seq;
     pa.num_blocks = num_blocks;
     pa.max_seqlen = max_seqlen_k;
+    pa.window = std::min(window, max_seqlen_k);
+    pa.sinks = std::min(sinks, max_seqlen_k);
     return cuda_status(launch_prefill(pa, static_cast<cudaStream_t>(stream)), name);
   }
   DecodeLaunch a;
@@ -298,7 +322,276 @@ int decode_impl(const void* q, const void* k_cache, const void* v_cache, const f
   a.fp8 = fp8 ? 1 : 0;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
+  if (window > 0) {
+    a.sel.select = 1;   // the same keys, and no overflow
+    a.sel.window = std::min(window, max_seqlen_k);
+    a.sel.sinks = std::min(sinks, max_seqlen_k);
+  }
   return cuda_status(launch_decode(a, static_cast<cudaStream_t>(stream)), name);
+}
+
+// Shared-prefix decode: the launches' parts of the workspace.  The prefix's partials are
+// those of one sequence with B * T query tokens; the own part's follow.
+struct SharedLayout {
+  int pre_chunk, pre_chunks;
+  size_t pre_lse_offset, own_offset, total;
+  DecodeLayout own;
+};
+
+bool shared_layout(int B, int T, int Hq, int Hkv, int d, int max_seqlen_k, int prefix_blocks, int num_splits, bool fp8,
+                   SharedLayout* out) {
+  if (B < 1 || T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || num_splits < 0 || prefix_blocks < 1) return false;
+  if (max_seqlen_k < 1 || max_seqlen_k > kMaxDecodeSeqlen || prefix_blocks > kMaxDecodeSeqlen / kPageTokens) return false;
+  if ((long long)B * T > INT32_MAX / 128 || Hq / Hkv > 128) return false;
+  const int P = prefix_blocks * kPageTokens;
+  if (max_seqlen_k - P < T) return false;
+  SharedLayout s;
+  if (!decode_layout(B, T, Hq, Hkv, d, max_seqlen_k - P, num_splits, fp8, &s.own)) return false;
+  s.pre_chunk = prefix_chunk_tokens(B * T, Hq / Hkv, Hkv, P, num_splits, fp8);
+  s.pre_chunks = (P + s.pre_chunk - 1) / s.pre_chunk;
+  const size_t rows = (size_t)Hkv * s.pre_chunks * B * T * (Hq / Hkv);
+  s.pre_lse_offset = (rows * d * sizeof(float) + 255) & ~size_t(255);
+  s.own_offset = (s.pre_lse_offset + rows * sizeof(float) + 255) & ~size_t(255);
+  s.total = s.own_offset + s.own.total;
+  *out = s;
+  return true;
+}
+
+int shared_impl(const void* q, const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                bool fp8, const int32_t* seqlens_k, const int32_t* page_table, int max_blocks_per_seq, int num_blocks,
+                const int32_t* prefix_table, int prefix_blocks, int max_seqlen_k, void* o, int o_dtype, float* lse,
+                int B, int T, int Hq, int Hkv, int d, float scale, int causal, int num_splits, void* workspace,
+                size_t workspace_bytes, void* stream, const char* name) {
+  if (!q || !k_cache || !v_cache || !seqlens_k || !page_table || !o) return ATTN_ERR_INVALID_ARG;
+  if (fp8 && (!k_scale || !v_scale)) return ATTN_ERR_INVALID_ARG;
+  if (B < 1 || T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || num_splits < 0) return ATTN_ERR_INVALID_ARG;
+  if (o_dtype != ATTN_F32 && o_dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !isfinite(scale) || (causal != 0 && causal != 1)) return ATTN_ERR_INVALID_ARG;
+  if (max_blocks_per_seq < 1 || num_blocks < 1 || prefix_blocks < 0 || prefix_blocks > max_blocks_per_seq)
+    return ATTN_ERR_INVALID_ARG;
+  if (prefix_blocks == 0)   // nothing shared: plain decode, with the same splitting and workspace rules
+    return decode_impl(q, k_cache, v_cache, k_scale, v_scale, fp8, seqlens_k, page_table, max_blocks_per_seq,
+                       num_blocks, 0, max_seqlen_k, o, o_dtype, lse, B, T, Hq, Hkv, d, scale, causal, num_splits,
+                       workspace, workspace_bytes, stream, name);
+  if (!prefix_table) return ATTN_ERR_INVALID_ARG;
+  if ((long long)num_blocks * kPageTokens > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+  const int capacity = (int)std::min<long long>((long long)max_blocks_per_seq * kPageTokens, INT32_MAX);
+  if (max_seqlen_k == 0) max_seqlen_k = std::min(capacity, kMaxDecodeSeqlen);
+  if (max_seqlen_k < 0 || max_seqlen_k > capacity) return ATTN_ERR_INVALID_ARG;
+  if (max_seqlen_k > kMaxDecodeSeqlen) return ATTN_ERR_UNSUPPORTED;
+  // every sequence holds the whole prefix and its T new tokens
+  if ((long long)prefix_blocks * kPageTokens + T > max_seqlen_k) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (Hq / Hkv > 128 || (fp8 && d != 128)) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)B * T > INT32_MAX / 128) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
+  SharedLayout s;
+  if (!shared_layout(B, T, Hq, Hkv, d, max_seqlen_k, prefix_blocks, num_splits, fp8, &s)) return ATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < s.total || !workspace || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
+  unsigned* st = status_ptr();
+  if (!st) return ATTN_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  // the prefix: one sequence whose queries are the whole batch's, every key visible to all
+  DecodeLaunch pre = {};
+  pre.q = q;
+  pre.k = k_cache;
+  pre.v = v_cache;
+  pre.page_table = prefix_table;
+  pre.max_blocks = prefix_blocks;
+  pre.num_blocks = num_blocks;
+  pre.max_seqlen = prefix_blocks * kPageTokens;
+  pre.B = 1;
+  pre.T = B * T;
+  pre.Hq = Hq;
+  pre.Hkv = Hkv;
+  pre.d = d;
+  pre.scale = scale;
+  pre.chunk = s.pre_chunk;
+  pre.max_chunks = s.pre_chunks;
+  pre.part_o = reinterpret_cast<float*>(ws);
+  pre.part_lse = reinterpret_cast<float*>(ws + s.pre_lse_offset);
+  pre.status = st;
+  pre.fp8 = fp8 ? 1 : 0;
+  pre.k_scale = k_scale;
+  pre.v_scale = v_scale;
+  pre.sel.select = 1;
+  pre.sel.fixed_len = prefix_blocks * kPageTokens;
+  // each sequence's own keys, and the merge of both parts
+  DecodeLaunch own = pre;
+  own.seqlens = seqlens_k;
+  own.page_table = page_table;
+  own.max_blocks = max_blocks_per_seq;
+  own.max_seqlen = max_seqlen_k;
+  own.o = o;
+  own.o_bf16 = o_dtype == ATTN_BF16;
+  own.lse = lse;
+  own.B = B;
+  own.T = T;
+  own.causal = causal;
+  own.chunk = s.own.chunk;
+  own.max_chunks = s.own.max_chunks;
+  own.part_o = reinterpret_cast<float*>(ws + s.own_offset);
+  own.part_lse = reinterpret_cast<float*>(ws + s.own_offset + s.own.lse_offset);
+  own.balanced = s.own.balanced;
+  own.n_chunks = s.own.n_chunks;
+  own.plan = s.own.balanced ? reinterpret_cast<int*>(ws + s.own_offset + s.own.plan_offset) : nullptr;
+  own.sel.fixed_len = 0;
+  own.sel.skip = prefix_blocks * kPageTokens;
+  own.pre_o = pre.part_o;
+  own.pre_lse = pre.part_lse;
+  own.pre_chunks = s.pre_chunks;
+  const int e = cuda_status(launch_decode_split(pre, static_cast<cudaStream_t>(stream)), name);
+  return e != ATTN_OK ? e : cuda_status(launch_decode(own, static_cast<cudaStream_t>(stream)), name);
+}
+
+int prefill_cache_impl(const void* q, const void* k_cache, const void* v_cache, const int32_t* seqlens_k,
+                       const int32_t* page_table, int max_blocks_per_seq, int num_blocks, int cache_capacity, void* o,
+                       int o_dtype, float* lse, int B, int Nq, int Hq, int Hkv, int d, float scale, int causal,
+                       bool windowed, int window, int sinks, void* stream, const char* name) {
+  if (!q || !k_cache || !v_cache || !seqlens_k || !o) return ATTN_ERR_INVALID_ARG;
+  if (B < 1 || Nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv) return ATTN_ERR_INVALID_ARG;
+  if (o_dtype != ATTN_F32 && o_dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !isfinite(scale) || (causal != 0 && causal != 1)) return ATTN_ERR_INVALID_ARG;
+  if (page_table) {
+    if (max_blocks_per_seq < 1 || num_blocks < 1) return ATTN_ERR_INVALID_ARG;
+    if ((long long)num_blocks * kPageTokens > INT32_MAX || (long long)max_blocks_per_seq * kPageTokens > INT32_MAX)
+      return ATTN_ERR_UNSUPPORTED;
+    if ((long long)max_blocks_per_seq * kPageTokens < Nq) return ATTN_ERR_INVALID_ARG;
+  } else {
+    if (cache_capacity < Nq) return ATTN_ERR_INVALID_ARG;
+  }
+  if (windowed && (window < 1 || sinks < 0)) return ATTN_ERR_INVALID_ARG;
+  const int max_keys = page_table ? max_blocks_per_seq * kPageTokens : cache_capacity;
+  if (windowed && max_keys > kMaxDecodeSeqlen) return ATTN_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
+  if ((long long)B * Nq * Hq > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+  unsigned* st = status_ptr();
+  if (!st) return ATTN_ERR_CUDA;
+  PrefillLaunch a;
+  a.q = q;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.o = o;
+  a.o_bf16 = o_dtype == ATTN_BF16;
+  a.lse = lse;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.N = Nq;
+  a.d = d;
+  a.scale = scale;
+  a.causal = causal;
+  a.status = st;
+  a.seqlens = seqlens_k;
+  a.page_table = page_table;
+  a.capacity = cache_capacity;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  if (windowed) {   // the same keys, and no overflow
+    a.window = std::min(window, max_keys);
+    a.sinks = std::min(sinks, max_keys);
+  }
+  return cuda_status(launch_prefill(a, static_cast<cudaStream_t>(stream)), name);
+}
+
+// Whether n1 bytes at p1 and n2 bytes at p2 share any.
+bool overlap(const void* p1, size_t n1, const void* p2, size_t n2) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p1), b = reinterpret_cast<uintptr_t>(p2);
+  return a < b + n2 && b < a + n1;
+}
+
+// The checks qk_norm_rope and kv_append_norm_rope share; fills the launch's common part.
+int norm_rope_args(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                   void* q_out, void* k_out, const void* q_weight, const void* k_weight, float eps, const float* rope,
+                   int rope_rows, int rot_dim, int interleaved, const int32_t* pos0, int B, int T, int Hq, int Hkv,
+                   int d, bool cached, NormRopeLaunch* out) {
+  if (!q || !k || !q_out || (cached ? !v : !k_out)) return ATTN_ERR_INVALID_ARG;
+  if (B < 1 || T < 1 || Hq < 1 || Hkv < 1 || rot_dim < 0 || (interleaved != 0 && interleaved != 1))
+    return ATTN_ERR_INVALID_ARG;
+  if ((rot_dim > 0) != (rope != nullptr) || (rot_dim > 0 && rope_rows < 1)) return ATTN_ERR_INVALID_ARG;
+  if ((q_weight || k_weight) && (!(eps > 0.f) || !isfinite(eps))) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (rot_dim > d) return ATTN_ERR_INVALID_ARG;
+  if (rot_dim % 16) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)B * T > INT32_MAX || (long long)Hq + 2LL * Hkv > INT32_MAX / 128) return ATTN_ERR_UNSUPPORTED;
+  if (q_stride < (int64_t)Hq * d || k_stride < (int64_t)Hkv * d || (cached && v_stride < (int64_t)Hkv * d) ||
+      q_stride % 8 || k_stride % 8 || (cached && v_stride % 8))
+    return ATTN_ERR_INVALID_ARG;
+  const int64_t n = (int64_t)B * T;
+  if (q_stride > INT64_MAX / 4 / n || k_stride > INT64_MAX / 4 / n || (cached && v_stride > INT64_MAX / 4 / n))
+    return ATTN_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, cached ? v : q, q_out, cached ? q_out : k_out, q_weight, k_weight, rope};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return ATTN_ERR_INVALID_ARG;
+  // an output may be exactly its own input; any other overlap would be read after it is written
+  const size_t qn = (size_t)(n * Hq * d) * 2, kn = (size_t)(n * Hkv * d) * 2;
+  auto span = [&](int64_t stride, int H) { return (size_t)((n - 1) * stride + (int64_t)H * d) * 2; };
+  auto clash = [&](const void* dst, size_t bytes, const void* src, int64_t stride, int H, bool own) {
+    if (own && dst == src && stride == (int64_t)H * d) return false;
+    return overlap(dst, bytes, src, span(stride, H));
+  };
+  if (clash(q_out, qn, q, q_stride, Hq, true) || clash(q_out, qn, k, k_stride, Hkv, false)) return ATTN_ERR_INVALID_ARG;
+  if (cached && clash(q_out, qn, v, v_stride, Hkv, false)) return ATTN_ERR_INVALID_ARG;
+  if (!cached && (clash(k_out, kn, q, q_stride, Hq, false) || clash(k_out, kn, k, k_stride, Hkv, true) ||
+                  overlap(q_out, qn, k_out, kn)))
+    return ATTN_ERR_INVALID_ARG;
+  NormRopeLaunch a = {};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.q_weight = static_cast<const __nv_bfloat16*>(q_weight);
+  a.k_weight = static_cast<const __nv_bfloat16*>(k_weight);
+  a.eps = eps;
+  a.rope = rope;
+  a.rope_rows = rope_rows;
+  a.rot = rot_dim;
+  a.interleaved = interleaved;
+  a.pos0 = pos0;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.cached = cached ? 1 : 0;
+  *out = a;
+  return ATTN_OK;
+}
+
+int append_norm_rope_impl(void* k_cache, void* v_cache, const void* q, const void* k_new, const void* v_new,
+                          int64_t q_stride, int64_t k_stride, int64_t v_stride, void* q_out, const float* k_scale,
+                          const float* v_scale, bool fp8, const void* q_weight, const void* k_weight, float eps,
+                          const float* rope, int rope_rows, int rot_dim, int interleaved, const int32_t* cache_lens,
+                          const int32_t* page_table, int max_blocks_per_seq, int num_blocks, int cache_capacity, int B,
+                          int T, int Hq, int Hkv, int d, void* stream, const char* name) {
+  if (!k_cache || !v_cache || !cache_lens) return ATTN_ERR_INVALID_ARG;
+  if (fp8 && (!k_scale || !v_scale)) return ATTN_ERR_INVALID_ARG;
+  if (page_table) {
+    if (max_blocks_per_seq < 1 || num_blocks < 1) return ATTN_ERR_INVALID_ARG;
+  } else if (cache_capacity < 1) {
+    return ATTN_ERR_INVALID_ARG;
+  }
+  NormRopeLaunch a;
+  const int e = norm_rope_args(q, k_new, v_new, q_stride, k_stride, v_stride, q_out, nullptr, q_weight, k_weight, eps,
+                               rope, rope_rows, rot_dim, interleaved, cache_lens, B, T, Hq, Hkv, d, true, &a);
+  if (e != ATTN_OK) return e;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return ATTN_ERR_INVALID_ARG;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.page_table = page_table;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.capacity = cache_capacity;
+  a.fp8 = fp8 ? 1 : 0;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  if (!(a.status = status_ptr())) return ATTN_ERR_CUDA;
+  return cuda_status(launch_norm_rope(a, static_cast<cudaStream_t>(stream)), name);
 }
 
 int append_impl(void* k_cache, void* v_cache, const void* k_new, const void* v_new, const float* k_scale,
@@ -347,44 +640,9 @@ int attn_prefill_cache(const void* q, const void* k_cache, const void* v_cache, 
                        const int32_t* page_table, int max_blocks_per_seq, int num_blocks, int cache_capacity, void* o,
                        int o_dtype, float* lse, int B, int Nq, int Hq, int Hkv, int d, float scale, int causal,
                        void* stream) {
-  if (!q || !k_cache || !v_cache || !seqlens_k || !o) return ATTN_ERR_INVALID_ARG;
-  if (B < 1 || Nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv) return ATTN_ERR_INVALID_ARG;
-  if (o_dtype != ATTN_F32 && o_dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !isfinite(scale) || (causal != 0 && causal != 1)) return ATTN_ERR_INVALID_ARG;
-  if (page_table) {
-    if (max_blocks_per_seq < 1 || num_blocks < 1) return ATTN_ERR_INVALID_ARG;
-    if ((long long)num_blocks * kPageTokens > INT32_MAX || (long long)max_blocks_per_seq * kPageTokens > INT32_MAX)
-      return ATTN_ERR_UNSUPPORTED;
-    if ((long long)max_blocks_per_seq * kPageTokens < Nq) return ATTN_ERR_INVALID_ARG;
-  } else {
-    if (cache_capacity < Nq) return ATTN_ERR_INVALID_ARG;
-  }
-  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
-  if ((long long)B * Nq * Hq > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
-  unsigned* st = status_ptr();
-  if (!st) return ATTN_ERR_CUDA;
-  PrefillLaunch a;
-  a.q = q;
-  a.k = k_cache;
-  a.v = v_cache;
-  a.o = o;
-  a.o_bf16 = o_dtype == ATTN_BF16;
-  a.lse = lse;
-  a.B = B;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.N = Nq;
-  a.d = d;
-  a.scale = scale;
-  a.causal = causal;
-  a.status = st;
-  a.seqlens = seqlens_k;
-  a.page_table = page_table;
-  a.capacity = cache_capacity;
-  a.max_blocks = max_blocks_per_seq;
-  a.num_blocks = num_blocks;
-  return cuda_status(launch_prefill(a, static_cast<cudaStream_t>(stream)), "attn_prefill_cache");
+  return prefill_cache_impl(q, k_cache, v_cache, seqlens_k, page_table, max_blocks_per_seq, num_blocks, cache_capacity,
+                            o, o_dtype, lse, B, Nq, Hq, Hkv, d, scale, causal, false, 0, 0, stream,
+                            "attn_prefill_cache");
 }
 
 int attn_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* seqlens_k,
@@ -413,6 +671,79 @@ int attn_decode_fp8(const void* q, const void* k_cache, const void* v_cache, con
   return decode_impl(q, k_cache, v_cache, k_scale, v_scale, true, seqlens_k, page_table, max_blocks_per_seq,
                      num_blocks, cache_capacity, max_seqlen_k, o, o_dtype, lse, B, T, Hq, Hkv, d, scale, causal,
                      num_splits, workspace, workspace_bytes, stream, "attn_decode_fp8");
+}
+
+int attn_prefill_window(const void* q, const void* k, const void* v, void* o, int o_dtype, float* lse, int B, int Hq,
+                        int Hkv, int N, int d, float scale, int window, int sinks, void* stream) {
+  return prefill_impl(q, k, v, o, o_dtype, lse, B, Hq, Hkv, N, d, scale, 1, true, window, sinks, stream,
+                      "attn_prefill_window");
+}
+
+int attn_prefill_cache_window(const void* q, const void* k_cache, const void* v_cache, const int32_t* seqlens_k,
+                              const int32_t* page_table, int max_blocks_per_seq, int num_blocks, int cache_capacity,
+                              void* o, int o_dtype, float* lse, int B, int Nq, int Hq, int Hkv, int d, float scale,
+                              int window, int sinks, void* stream) {
+  return prefill_cache_impl(q, k_cache, v_cache, seqlens_k, page_table, max_blocks_per_seq, num_blocks, cache_capacity,
+                            o, o_dtype, lse, B, Nq, Hq, Hkv, d, scale, 1, true, window, sinks, stream,
+                            "attn_prefill_cache_window");
+}
+
+size_t attn_decode_window_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int max_seqlen_k, int window, int sinks,
+                                          int num_splits) {
+  if (window < 1 || sinks < 0 || T < 1 || max_seqlen_k < 1 || max_seqlen_k > kMaxDecodeSeqlen) return 0;
+  return attn_decode_workspace_bytes(B, T, Hq, Hkv, d, window_max_keys(max_seqlen_k, T, window, sinks), num_splits);
+}
+
+int attn_decode_window(const void* q, const void* k_cache, const void* v_cache, const int32_t* seqlens_k,
+                       const int32_t* page_table, int max_blocks_per_seq, int num_blocks, int cache_capacity,
+                       int max_seqlen_k, void* o, int o_dtype, float* lse, int B, int T, int Hq, int Hkv, int d,
+                       float scale, int window, int sinks, int num_splits, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  return decode_impl(q, k_cache, v_cache, nullptr, nullptr, false, seqlens_k, page_table, max_blocks_per_seq,
+                     num_blocks, cache_capacity, max_seqlen_k, o, o_dtype, lse, B, T, Hq, Hkv, d, scale, 1, num_splits,
+                     workspace, workspace_bytes, stream, "attn_decode_window", false, window, sinks);
+}
+
+int attn_decode_window_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, const int32_t* seqlens_k, const int32_t* page_table,
+                           int max_blocks_per_seq, int num_blocks, int cache_capacity, int max_seqlen_k, void* o,
+                           int o_dtype, float* lse, int B, int T, int Hq, int Hkv, int d, float scale, int window,
+                           int sinks, int num_splits, void* workspace, size_t workspace_bytes, void* stream) {
+  if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  return decode_impl(q, k_cache, v_cache, k_scale, v_scale, true, seqlens_k, page_table, max_blocks_per_seq, num_blocks,
+                     cache_capacity, max_seqlen_k, o, o_dtype, lse, B, T, Hq, Hkv, d, scale, 1, num_splits, workspace,
+                     workspace_bytes, stream, "attn_decode_window_fp8", false, window, sinks);
+}
+
+size_t attn_decode_shared_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int max_seqlen_k, int prefix_blocks,
+                                          int num_splits) {
+  if (prefix_blocks == 0) return attn_decode_workspace_bytes(B, T, Hq, Hkv, d, max_seqlen_k, num_splits);
+  SharedLayout s, s8;   // enough for either cache type, as attn_decode_workspace_bytes
+  if (!shared_layout(B, T, Hq, Hkv, d, max_seqlen_k, prefix_blocks, num_splits, false, &s)) return 0;
+  if (!shared_layout(B, T, Hq, Hkv, d, max_seqlen_k, prefix_blocks, num_splits, true, &s8)) return 0;
+  return std::max(s.total, s8.total);
+}
+
+int attn_decode_shared(const void* q, const void* k_cache, const void* v_cache, const int32_t* seqlens_k,
+                       const int32_t* page_table, int max_blocks_per_seq, int num_blocks, const int32_t* prefix_table,
+                       int prefix_blocks, int max_seqlen_k, void* o, int o_dtype, float* lse, int B, int T, int Hq,
+                       int Hkv, int d, float scale, int causal, int num_splits, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  return shared_impl(q, k_cache, v_cache, nullptr, nullptr, false, seqlens_k, page_table, max_blocks_per_seq, num_blocks,
+                     prefix_table, prefix_blocks, max_seqlen_k, o, o_dtype, lse, B, T, Hq, Hkv, d, scale, causal,
+                     num_splits, workspace, workspace_bytes, stream, "attn_decode_shared");
+}
+
+int attn_decode_shared_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, const int32_t* seqlens_k, const int32_t* page_table,
+                           int max_blocks_per_seq, int num_blocks, const int32_t* prefix_table, int prefix_blocks,
+                           int max_seqlen_k, void* o, int o_dtype, float* lse, int B, int T, int Hq, int Hkv, int d,
+                           float scale, int causal, int num_splits, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  return shared_impl(q, k_cache, v_cache, k_scale, v_scale, true, seqlens_k, page_table, max_blocks_per_seq, num_blocks,
+                     prefix_table, prefix_blocks, max_seqlen_k, o, o_dtype, lse, B, T, Hq, Hkv, d, scale, causal,
+                     num_splits, workspace, workspace_bytes, stream, "attn_decode_shared_fp8");
 }
 
 int kv_append(void* k_cache, void* v_cache, const void* k_new, const void* v_new, const int32_t* cache_lens,
@@ -451,6 +782,47 @@ int kv_append_fp8(void* k_cache, void* v_cache, const void* k_new, const void* v
                   int num_blocks, int cache_capacity, int B, int T, int Hkv, int d, void* stream) {
   return append_impl(k_cache, v_cache, k_new, v_new, k_scale, v_scale, true, cache_lens, page_table,
                      max_blocks_per_seq, num_blocks, cache_capacity, B, T, Hkv, d, stream, "kv_append_fp8");
+}
+
+int qk_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride, void* q_out, void* k_out,
+                 const void* q_weight, const void* k_weight, float eps, const float* rope, int rope_rows, int rot_dim,
+                 int interleaved, const int32_t* pos0, int B, int T, int Hq, int Hkv, int d, void* stream) {
+  NormRopeLaunch a;
+  const int e = norm_rope_args(q, k, nullptr, q_stride, k_stride, 0, q_out, k_out, q_weight, k_weight, eps, rope,
+                               rope_rows, rot_dim, interleaved, pos0, B, T, Hq, Hkv, d, false, &a);
+  if (e != ATTN_OK) return e;
+  if (!(a.status = status_ptr())) return ATTN_ERR_CUDA;
+  return cuda_status(launch_norm_rope(a, static_cast<cudaStream_t>(stream)), "qk_norm_rope");
+}
+
+int kv_append_norm_rope(void* k_cache, void* v_cache, const void* q, const void* k_new, const void* v_new,
+                        int64_t q_stride, int64_t k_stride, int64_t v_stride, void* q_out, const void* q_weight,
+                        const void* k_weight, float eps, const float* rope, int rope_rows, int rot_dim,
+                        int interleaved, const int32_t* cache_lens, const int32_t* page_table, int max_blocks_per_seq,
+                        int num_blocks, int cache_capacity, int B, int T, int Hq, int Hkv, int d, void* stream) {
+  return append_norm_rope_impl(k_cache, v_cache, q, k_new, v_new, q_stride, k_stride, v_stride, q_out, nullptr, nullptr,
+                               false, q_weight, k_weight, eps, rope, rope_rows, rot_dim, interleaved, cache_lens,
+                               page_table, max_blocks_per_seq, num_blocks, cache_capacity, B, T, Hq, Hkv, d, stream,
+                               "kv_append_norm_rope");
+}
+
+int kv_append_norm_rope_fp8(void* k_cache, void* v_cache, const void* q, const void* k_new, const void* v_new,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride, void* q_out, const float* k_scale,
+                            const float* v_scale, const void* q_weight, const void* k_weight, float eps,
+                            const float* rope, int rope_rows, int rot_dim, int interleaved, const int32_t* cache_lens,
+                            const int32_t* page_table, int max_blocks_per_seq, int num_blocks, int cache_capacity,
+                            int B, int T, int Hq, int Hkv, int d, void* stream) {
+  return append_norm_rope_impl(k_cache, v_cache, q, k_new, v_new, q_stride, k_stride, v_stride, q_out, k_scale, v_scale,
+                               true, q_weight, k_weight, eps, rope, rope_rows, rot_dim, interleaved, cache_lens,
+                               page_table, max_blocks_per_seq, num_blocks, cache_capacity, B, T, Hq, Hkv, d, stream,
+                               "kv_append_norm_rope_fp8");
+}
+
+int rope_table_fill(float* table, int rows, int rot_dim, double theta, void* stream) {
+  if (!table || rows < 1 || rot_dim < 2 || rot_dim % 2 || !(theta > 0.0) || !isfinite(theta))
+    return ATTN_ERR_INVALID_ARG;
+  return cuda_status(launch_rope_table(table, rows, rot_dim, theta, static_cast<cudaStream_t>(stream)),
+                     "rope_table_fill");
 }
 
 }  // extern "C"

@@ -32,6 +32,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "ptx.cuh"
 #include "split.cuh"
@@ -68,7 +70,7 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
   return pack_f16x2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-template <int D, int MT, bool PAGED, bool FP8>
+template <int D, int MT, bool PAGED, bool FP8, bool SEL>
 __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, MT, FP8>::kMinBlocks)
     decode_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const SplitParams p) {
@@ -84,11 +86,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
   const int lane = threadIdx.x & 31;
   const int c = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
 
-  const int L = p.seqlens[b];
-  if (seqlen_bad(L, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks)) {
+  const SeqKeys sk = seq_keys<SEL>(p.sel, p.seqlens, b, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
+  if (sk.bad) {
     if (threadIdx.x == 0 && c == 0 && g == 0) atomicOr(p.status, DEV_SEQLEN);
     return;   // the combine kernel writes NaN rows for this sequence
   }
+  const int L = sk.L;
   const int tok_begin = c * p.chunk;
   if (tok_begin >= L) return;
   const int tok_end = min(tok_begin + p.chunk, L);
@@ -118,8 +121,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
 
   if (warp == C::kConsumerWarps) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) produce_split_tiles<C, PAGED>(smem, full, empty, &tmK, &tmV, p, b, g, tok_begin, tok_end, n_tiles,
-                                                abort_flag);
+    if (lane == 0) produce_split_tiles<C, PAGED, SEL>(smem, full, empty, &tmK, &tmV, p, b, g, tok_begin, tok_end,
+                                                     n_tiles, sk, abort_flag);
     return;
   }
 
@@ -135,6 +138,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
     if (r0 < p.R) end0 = L - p.T + r0 / p.G + 1;
     if (r1 < p.R) end1 = L - p.T + r1 / p.G + 1;
   }
+  // SEL: a row sees keys below `sinks` and from its window's first key on; no row sees
+  // [sinks, dead_end), whose V rows are zeroed like those past L (they may hold anything)
+  const int lo0 = SEL ? end0 - p.sel.window : 0, lo1 = SEL ? end1 - p.sel.window : 0;
+  const int dead_end = SEL && p.causal ? L - p.T + 1 - p.sel.window : 0;
+  auto dead = [&](int tok) { return tok >= L || (SEL && tok >= p.sel.sinks && tok < dead_end); };
+  auto has_dead = [&](int tok0) {   // among tok0 .. tok0 + 15
+    return tok0 + 16 > L || (SEL && tok0 < dead_end && tok0 + 16 > p.sel.sinks);
+  };
 
   // Q fragments (A operand, 16 x D, row-major) straight from global memory.
   uint32_t qa[D / 16][4];
@@ -239,24 +250,24 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
     uint32_t vb[FP8 ? 1 : D / 16][4];
     uint32_t vw[FP8 ? 4 : 1][4];   // FP8: 16 bytes (d = 16 gid .. 16 gid + 15) of keys 2tig, 2tig+1, 2tig+8, 2tig+9
     if constexpr (FP8) {
-      const bool tail = tok_base + 16 > L;
+      const bool tail = has_dead(tok_base);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int key = 2 * tig + (i & 1) + 8 * (i >> 1);
         const int vrow = wsub * 16 + key;
         uint4 x = lds128(vbase + vrow * 128 + ((gid ^ (vrow & 7)) << 4));
-        if (tail && tok_base + key >= L) x = make_uint4(0u, 0u, 0u, 0u);
+        if (tail && dead(tok_base + key)) x = make_uint4(0u, 0u, 0u, 0u);
         vw[i][0] = x.x;
         vw[i][1] = x.y;
         vw[i][2] = x.z;
         vw[i][3] = x.w;
       }
     } else {
-      const bool tail = tok_base + 16 > L;
+      const bool tail = has_dead(tok_base);
       const int vrow = wsub * 16 + (lm & 1) * 8 + lr;
       const int ta = tok_base + tig * 2, tb = ta + 8;
-      const uint32_t keep_a = ((ta < L) ? 0x0000ffffu : 0u) | ((ta + 1 < L) ? 0xffff0000u : 0u);
-      const uint32_t keep_b = ((tb < L) ? 0x0000ffffu : 0u) | ((tb + 1 < L) ? 0xffff0000u : 0u);
+      const uint32_t keep_a = (dead(ta) ? 0u : 0x0000ffffu) | (dead(ta + 1) ? 0u : 0xffff0000u);
+      const uint32_t keep_b = (dead(tb) ? 0u : 0x0000ffffu) | (dead(tb + 1) ? 0u : 0xffff0000u);
 #pragma unroll
       for (int nn = 0; nn < D / 16; ++nn) {
         const int chunk16 = nn * 2 + (lm >> 1);
@@ -283,7 +294,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
       for (int e = 0; e < 4; ++e) {
         const int tok = tok_base + n * 8 + tig * 2 + (e & 1);
         const int end = (e < 2) ? end0 : end1;
-        const float v = (tok < end) ? sacc[n][e] * scale_log2 : -INFINITY;
+        bool seen = tok < end;
+        if constexpr (SEL) seen = seen && (tok >= ((e < 2) ? lo0 : lo1) || tok < p.sel.sinks);
+        const float v = seen ? sacc[n][e] * scale_log2 : -INFINITY;
         sacc[n][e] = v;
         if (e < 2) mx0 = fmaxf(mx0, v); else mx1 = fmaxf(mx1, v);
       }
@@ -468,11 +481,19 @@ __device__ __forceinline__ void accumulate(float (&acc)[kPer], float w, float4 x
 // dependent memory round trips.  kBatch: partial loads in flight per lane -- 8 for
 // long decode (many chunks per row), 2 for launches of at most two chunks (many rows,
 // as in a prompt chunk), where a small register footprint buys five CTAs per SM.
-template <int D, int kBatch>
+// SEL: the sequences' selected keys.  With a shared prefix (pre.chunks > 0) the row's
+// first pre.chunks chunks are the prefix's partials.
+struct PrefixParts {
+  const float* o;
+  const float* lse;
+  int chunks, rows;   // rows per chunk: B * T * G
+};
+template <int D, int kBatch, bool SEL>
 __global__ void __launch_bounds__(256, kBatch >= 8 ? 2 : 5) decode_combine_kernel(const float* __restrict__ part_o,
                                                              const float* __restrict__ part_lse,
                                                              const int32_t* __restrict__ seqlens, void* o, int o_bf16,
-                                                             float* lse, SplitParams p, int B, int paged, int wpr) {
+                                                             float* lse, SplitParams p, int B, int paged, int wpr,
+                                                             PrefixParts pre) {
   constexpr int kPer = D / 32;    // output columns per lane
   __shared__ float4 red[8][32];   // one float4 per lane of each of the 8 warps
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -487,8 +508,9 @@ __global__ void __launch_bounds__(256, kBatch >= 8 ? 2 : 5) decode_combine_kerne
   bool bad = true;
   int nc = 0, L = 0;
   if (live) {
-    L = seqlens[b];
-    bad = seqlen_bad(L, p.T, p.max_seqlen, paged != 0, p.capacity, p.max_blocks);
+    const SeqKeys sk = seq_keys<SEL>(p.sel, seqlens, b, p.T, p.max_seqlen, paged != 0, p.capacity, p.max_blocks);
+    L = sk.L;
+    bad = sk.bad;
     if (!bad && !p.balanced) nc = (L + p.chunk - 1) / p.chunk;
   }
   grid_dependency_wait();   // launched early (programmatic dependent launch): the partials are ready after this
@@ -499,6 +521,8 @@ __global__ void __launch_bounds__(256, kBatch >= 8 ? 2 : 5) decode_combine_kerne
     nc = (L + chunk_b - 1) / chunk_b;
     item0 = (size_t)p.Hkv * first + (size_t)g * n_b;
   }
+  const int npre = SEL && nc > 0 ? pre.chunks : 0;
+  nc += npre;
 
   float acc[kPer];
 #pragma unroll
@@ -508,18 +532,34 @@ __global__ void __launch_bounds__(256, kBatch >= 8 ? 2 : 5) decode_combine_kerne
     const float* lse0 = part_lse + item0 * p.R + r;            // chunk c at lse0[c * R]
     const float* src0 = part_o + (item0 * p.R + r) * D + lane * kPer;
     const size_t cstride = (size_t)p.R * D;                    // floats between consecutive chunks of this row
+    // row of the shared prefix's partials: the whole batch's rows of KV head g, in order
+    const size_t pre0 = SEL ? (size_t)g * pre.chunks * pre.rows + (size_t)b * p.R + r : 0;
+    auto chunk_lse = [&](int c) -> const float* {
+      if constexpr (SEL) {
+        if (c < npre) return pre.lse + pre0 + (size_t)c * pre.rows;
+        c -= npre;
+      }
+      return lse0 + (size_t)c * p.R;
+    };
+    auto chunk_o = [&](int c) -> const float* {
+      if constexpr (SEL) {
+        if (c < npre) return pre.o + (pre0 + (size_t)c * pre.rows) * D + lane * kPer;
+        c -= npre;
+      }
+      return src0 + (size_t)c * cstride;
+    };
     const int n0 = min(nc, 32);
-    const float lc0 = lane < n0 ? __ldg(lse0 + (size_t)lane * p.R) : -INFINITY;
+    const float lc0 = lane < n0 ? __ldg(chunk_lse(lane)) : -INFINITY;
     float4 x[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int c = wi + u * wpr;
-      x[u] = c < n0 ? load_part<kPer>(src0 + (size_t)c * cstride) : make_float4(0.f, 0.f, 0.f, 0.f);
+      x[u] = c < n0 ? load_part<kPer>(chunk_o(c)) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     // log-sum-exp over the chunks: every lane keeps a (max, sum) pair, then the pairs merge
     float m = lc0, sum = lc0 == -INFINITY ? 0.f : 1.f;
     for (int c = 32 + lane; c < nc; c += 32) {
-      const float lc = __ldg(lse0 + (size_t)c * p.R);
+      const float lc = __ldg(chunk_lse(c));
       if (lc == -INFINITY) continue;
       if (lc > m) {
         sum = sum * expf(m - lc) + 1.f;
@@ -548,14 +588,14 @@ __global__ void __launch_bounds__(256, kBatch >= 8 ? 2 : 5) decode_combine_kerne
       const int n = min(32, nc - g0);
       const int first = g0 == 0 ? wi + kBatch * wpr : wi;
       if (first >= n) continue;
-      const float lc = g0 == 0 ? lc0 : (lane < n ? __ldg(lse0 + (size_t)(g0 + lane) * p.R) : -INFINITY);
+      const float lc = g0 == 0 ? lc0 : (lane < n ? __ldg(chunk_lse(g0 + lane)) : -INFINITY);
       const float wl = lc == -INFINITY ? 0.f : expf(lc - lse_row);
       for (int j0 = first; j0 < n; j0 += kBatch * wpr) {
         float4 y[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
           const int j = j0 + u * wpr;
-          y[u] = j < n ? load_part<kPer>(src0 + (size_t)(g0 + j) * cstride) : make_float4(0.f, 0.f, 0.f, 0.f);
+          y[u] = j < n ? load_part<kPer>(chunk_o(g0 + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
@@ -607,16 +647,53 @@ __global__ void __launch_bounds__(256, kBatch >= 8 ? 2 : 5) decode_combine_kerne
   if (lse && lane == 0) lse[((size_t)b * p.Hq + h) * p.T + t] = lse_row;
 }
 
-template <int D, int MT, bool PAGED, bool FP8 = false>
-cudaError_t run_split(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int B,
+template <int D, int MT, bool PAGED, bool FP8, bool SEL>
+cudaError_t run_split_as(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int B,
                       cudaStream_t stream) {
   using C = DecodeCfg<D, MT, FP8>;
-  auto kern = decode_split_kernel<D, MT, PAGED, FP8>;
+  auto kern = decode_split_kernel<D, MT, PAGED, FP8, SEL>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   dim3 grid(sp.max_chunks, sp.Hkv, B);
   kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(tk, tv, sp);
   return cudaGetLastError();
+}
+
+template <int D, int MT, bool PAGED, bool FP8 = false>
+cudaError_t run_split(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int B,
+                      cudaStream_t stream) {
+  return sp.sel.select ? run_split_as<D, MT, PAGED, FP8, true>(tk, tv, sp, B, stream)
+                       : run_split_as<D, MT, PAGED, FP8, false>(tk, tv, sp, B, stream);
+}
+
+SplitParams split_params(const DecodeLaunch& a) {
+  const int G = a.Hq / a.Hkv;
+  SplitParams sp;
+  sp.q = static_cast<const __nv_bfloat16*>(a.q);
+  sp.k_scale = a.k_scale;
+  sp.v_scale = a.v_scale;
+  sp.seqlens = a.seqlens;
+  sp.page_table = a.page_table;
+  sp.part_o = a.part_o;
+  sp.part_lse = a.part_lse;
+  sp.status = a.status;
+  sp.T = a.T;
+  sp.Hq = a.Hq;
+  sp.Hkv = a.Hkv;
+  sp.G = G;
+  sp.R = G * a.T;
+  sp.chunk = a.chunk;
+  sp.max_chunks = a.max_chunks;
+  sp.capacity = a.capacity;
+  sp.max_blocks = a.max_blocks;
+  sp.num_blocks = a.num_blocks;
+  sp.max_seqlen = a.max_seqlen;
+  sp.scale_log2 = a.scale * kLog2e;
+  sp.causal = a.causal;
+  sp.balanced = a.balanced;
+  sp.plan = a.plan;
+  sp.sel = a.sel;
+  return sp;
 }
 
 }  // namespace
@@ -648,6 +725,10 @@ int decode_chunk_tokens(int B, int T, int G, int Hkv, int max_seqlen, int num_sp
   return chunk < kDecodeTcTile ? kDecodeTcTile : chunk;
 }
 
+int prefix_chunk_tokens(int tokens, int G, int Hkv, int prefix, int num_splits, bool fp8) {
+  return decode_chunk_tokens(1, tokens, G, Hkv, prefix, num_splits, fp8);
+}
+
 int decode_balanced_chunks(int B, int Hkv) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -659,38 +740,15 @@ int decode_balanced_chunks(int B, int Hkv) {
   return n > B ? n : B;
 }
 
-cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream) {
+cudaError_t launch_decode_split(const DecodeLaunch& a, cudaStream_t stream) {
   const bool paged = a.page_table != nullptr;
-  const int G = a.Hq / a.Hkv, R = G * a.T;
-  SplitParams sp;
-  sp.q = static_cast<const __nv_bfloat16*>(a.q);
-  sp.k_scale = a.k_scale;
-  sp.v_scale = a.v_scale;
-  sp.seqlens = a.seqlens;
-  sp.page_table = a.page_table;
-  sp.part_o = a.part_o;
-  sp.part_lse = a.part_lse;
-  sp.status = a.status;
-  sp.T = a.T;
-  sp.Hq = a.Hq;
-  sp.Hkv = a.Hkv;
-  sp.G = G;
-  sp.R = R;
-  sp.chunk = a.chunk;
-  sp.max_chunks = a.max_chunks;
-  sp.capacity = a.capacity;
-  sp.max_blocks = a.max_blocks;
-  sp.num_blocks = a.num_blocks;
-  sp.max_seqlen = a.max_seqlen;
-  sp.scale_log2 = a.scale * kLog2e;
-  sp.causal = a.causal;
-  sp.balanced = a.balanced;
-  sp.plan = a.plan;
+  const int R = a.Hq / a.Hkv * a.T;
+  const SplitParams sp = split_params(a);
 
   // K/V viewed as 3-D {d, Hkv, rows}: rows = B * capacity (contiguous) or num_blocks * 16 (paged)
   const uint64_t rows = paged ? (uint64_t)a.num_blocks * kPageTokens : (uint64_t)a.B * a.capacity;
   const bool tc = decode_uses_tc(R, a.fp8 != 0);
-  const uint32_t box_rows = paged ? kPageTokens : (tc ? kDecodeTcTile : kDecodeTile);
+  const uint32_t box_rows = paged || a.sel.select ? kPageTokens : (tc ? kDecodeTcTile : kDecodeTile);
   CUtensorMap tk, tv;
   const int eb = a.fp8 ? 1 : 2;   // bytes per cached element
   const uint64_t s1 = (uint64_t)a.d * eb, s2 = (uint64_t)a.Hkv * a.d * eb;
@@ -704,7 +762,7 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream) {
     e = launch_decode_tc(a, tk, tv, stream);   // bf16 above 16 rows per KV head, FP8 above 32
   } else if (a.fp8) {
     // api.cu admits FP8 caches with d == 128 only
-    if (R <= 8) e = launch_decode_fp8_rows8(tk, tv, sp, a.B, paged, stream);
+    if (R <= 8) e = launch_decode_fp8_rows8(tk, tv, sp, a.B, paged, a.sel.select != 0, stream);
     else if (R <= 16) e = paged ? run_split<128, 1, true, true>(tk, tv, sp, a.B, stream)
                            : run_split<128, 1, false, true>(tk, tv, sp, a.B, stream);
     else e = paged ? run_split<128, 2, true, true>(tk, tv, sp, a.B, stream)
@@ -714,13 +772,20 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream) {
   } else {
     e = paged ? run_split<64, 1, true>(tk, tv, sp, a.B, stream) : run_split<64, 1, false>(tk, tv, sp, a.B, stream);
   }
+  return e;
+}
+
+cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream) {
+  cudaError_t e = launch_decode_split(a, stream);
   if (e != cudaSuccess) return e;
+  const SplitParams sp = split_params(a);
 
   // the combine kernel is launched as a programmatic dependent of the split kernel:
   // it starts launching while the split kernel's last CTAs finish and waits for them
   // warps per output row: enough that each warp merges at most four chunks
   int wpr = 1;
-  while (wpr < 8 && wpr * 4 < sp.max_chunks) wpr *= 2;
+  const int row_chunks = sp.max_chunks + a.pre_chunks;
+  while (wpr < 8 && wpr * 4 < row_chunks) wpr *= 2;
   const long long rows_out = (long long)a.B * a.T * a.Hq;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((rows_out * wpr + 7) / 8));
@@ -732,12 +797,17 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const int paged_i = paged ? 1 : 0;
-  const bool light = sp.max_chunks <= 2;
-  auto kern = a.d == 128 ? (light ? decode_combine_kernel<128, 2> : decode_combine_kernel<128, 8>)
-                         : (light ? decode_combine_kernel<64, 2> : decode_combine_kernel<64, 8>);
+  const int paged_i = a.page_table != nullptr ? 1 : 0;
+  const bool light = row_chunks <= 2;
+  const PrefixParts pre = {a.pre_o, a.pre_lse, a.pre_chunks, a.B * sp.R};
+  auto pick = [&](auto sel) {
+    constexpr bool S = decltype(sel)::value;
+    return a.d == 128 ? (light ? decode_combine_kernel<128, 2, S> : decode_combine_kernel<128, 8, S>)
+                      : (light ? decode_combine_kernel<64, 2, S> : decode_combine_kernel<64, 8, S>);
+  };
+  auto kern = a.sel.select ? pick(std::true_type{}) : pick(std::false_type{});
   e = cudaLaunchKernelEx(&cfg, kern, (const float*)a.part_o, (const float*)a.part_lse, a.seqlens, a.o, a.o_bf16,
-                         a.lse, sp, a.B, paged_i, wpr);
+                         a.lse, sp, a.B, paged_i, wpr, pre);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

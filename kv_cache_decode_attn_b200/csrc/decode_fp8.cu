@@ -61,7 +61,7 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
   return pack_f16x2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-template <bool PAGED>
+template <bool PAGED, bool SEL>
 __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
     decode_fp8_st_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const SplitParams p) {
@@ -77,11 +77,12 @@ __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
   const int lane = threadIdx.x & 31;
   const int c = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
 
-  const int L = p.seqlens[b];
-  if (seqlen_bad(L, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks)) {
+  const SeqKeys sk = seq_keys<SEL>(p.sel, p.seqlens, b, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
+  if (sk.bad) {
     if (threadIdx.x == 0 && c == 0 && g == 0) atomicOr(p.status, DEV_SEQLEN);
     return;   // the combine kernel writes NaN rows for this sequence
   }
+  const int L = sk.L;
   const int tok_begin = c * p.chunk;
   if (tok_begin >= L) return;
   const int tok_end = min(tok_begin + p.chunk, L);
@@ -106,8 +107,8 @@ __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
   __syncthreads();
 
   if (warp == C::kConsumerWarps) {
-    if (lane == 0) produce_split_tiles<C, PAGED>(smem, full, empty, &tmK, &tmV, p, b, g, tok_begin, tok_end, n_tiles,
-                                                abort_flag);
+    if (lane == 0) produce_split_tiles<C, PAGED, SEL>(smem, full, empty, &tmK, &tmV, p, b, g, tok_begin, tok_end,
+                                                     n_tiles, sk, abort_flag);
     return;
   }
 
@@ -133,6 +134,15 @@ __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
   const int r0 = 2 * tig, r1 = r0 + 1;
   const int end0 = r0 < p.R ? (p.causal ? L - p.T + r0 / p.G + 1 : L) : 0;
   const int end1 = r1 < p.R ? (p.causal ? L - p.T + r1 / p.G + 1 : L) : 0;
+
+  // SEL: a row sees keys below `sinks` and from its window's first key on; no row sees
+  // [sinks, dead_end), whose V rows are zeroed like those past L (they may hold anything)
+  const int lo0 = SEL ? end0 - p.sel.window : 0, lo1 = SEL ? end1 - p.sel.window : 0;
+  const int dead_end = SEL && p.causal ? L - p.T + 1 - p.sel.window : 0;
+  auto dead = [&](int tok) { return tok >= L || (SEL && tok >= p.sel.sinks && tok < dead_end); };
+  auto seen = [&](int tok, int end, int lo) {
+    return tok < end && (!SEL || tok >= lo || tok < p.sel.sinks);
+  };
 
   float o[8][4];
 #pragma unroll
@@ -178,13 +188,13 @@ __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
     //      softmax; keys at or past L may hold any bytes, so their rows are zeroed
     uint32_t vw[4][4];
     {
-      const bool tail = tok_base + 16 > L;
+      const bool tail = tok_base + 16 > L || (SEL && tok_base < dead_end && tok_base + 16 > p.sel.sinks);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int key = 2 * tig + (q & 1) + 8 * (q >> 1);
         const int vrow = wsub * 16 + key;
         uint4 x = lds128(vbase + vrow * 128 + ((gid ^ (vrow & 7)) << 4));
-        if (tail && tok_base + key >= L) x = make_uint4(0u, 0u, 0u, 0u);
+        if (tail && dead(tok_base + key)) x = make_uint4(0u, 0u, 0u, 0u);
         vw[q][0] = x.x;
         vw[q][1] = x.y;
         vw[q][2] = x.z;
@@ -194,10 +204,10 @@ __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
 
     // ---- online softmax over this warp's keys for query rows r0, r1 (base 2, lazy rescale)
     const int ka = tok_base + gid, kb = ka + 8;
-    const float v00 = (ka < end0) ? sacc[0] * scale_log2 : -INFINITY;   // key gid,     row r0
-    const float v01 = (ka < end1) ? sacc[1] * scale_log2 : -INFINITY;   // key gid,     row r1
-    const float v10 = (kb < end0) ? sacc[2] * scale_log2 : -INFINITY;   // key gid + 8, row r0
-    const float v11 = (kb < end1) ? sacc[3] * scale_log2 : -INFINITY;   // key gid + 8, row r1
+    const float v00 = seen(ka, end0, lo0) ? sacc[0] * scale_log2 : -INFINITY;   // key gid,     row r0
+    const float v01 = seen(ka, end1, lo1) ? sacc[1] * scale_log2 : -INFINITY;   // key gid,     row r1
+    const float v10 = seen(kb, end0, lo0) ? sacc[2] * scale_log2 : -INFINITY;   // key gid + 8, row r0
+    const float v11 = seen(kb, end1, lo1) ? sacc[3] * scale_log2 : -INFINITY;   // key gid + 8, row r1
     float mx0 = fmaxf(v00, v10), mx1 = fmaxf(v01, v11);
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
@@ -311,9 +321,9 @@ __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
   }
 }
 
-template <bool PAGED>
+template <bool PAGED, bool SEL>
 cudaError_t run(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int B, cudaStream_t stream) {
-  auto kern = decode_fp8_st_kernel<PAGED>;
+  auto kern = decode_fp8_st_kernel<PAGED, SEL>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Fp8StCfg::kSmemBytes);
   if (e != cudaSuccess) return e;
   dim3 grid(sp.max_chunks, sp.Hkv, B);
@@ -324,8 +334,9 @@ cudaError_t run(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams&
 }  // namespace
 
 cudaError_t launch_decode_fp8_rows8(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int B,
-                                    bool paged, cudaStream_t stream) {
-  return paged ? run<true>(tk, tv, sp, B, stream) : run<false>(tk, tv, sp, B, stream);
+                                    bool paged, bool sel, cudaStream_t stream) {
+  if (sel) return paged ? run<true, true>(tk, tv, sp, B, stream) : run<false, true>(tk, tv, sp, B, stream);
+  return paged ? run<true, false>(tk, tv, sp, B, stream) : run<false, false>(tk, tv, sp, B, stream);
 }
 
 }  // namespace kvattn

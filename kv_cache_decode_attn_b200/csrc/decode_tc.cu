@@ -40,6 +40,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "split.cuh"
 
 namespace kvattn {
 namespace {
@@ -129,6 +130,7 @@ struct TcParams {
   int causal;
   int balanced, n_chunks, B;   // balanced split: n_chunks over the batch (per KV head)
   int* plan;                   // [B, 3] written by CTA 0 for the combine kernel
+  KeySelect sel;               // SEL instances: which keys of a sequence the launch reads
 };
 
 // Balanced split: the chunks of this launch and this CTA's (sequence, KV head, chunk),
@@ -138,16 +140,25 @@ struct TcParams {
 // length is ceil(L_b / n_b) rounded up to whole 64-token tiles.  Linear block index
 // i = Hkv * first_b + g * n_b + c is the partial's index.  Lengths outside
 // [1, max_seqlen] count as clamped (such a sequence's rows are reported invalid anyway).
+// SEL: L_b is the sequence's number of selected keys (1 for an invalid length).
 struct BalancedItem {
   int b, g, c, chunk;
 };
+template <bool SEL, bool PAGED>
 __device__ __forceinline__ BalancedItem balanced_item(const TcParams& p, int* plan_smem) {
   int* len = plan_smem;                                   // [B]
   int* base = plan_smem + kBalancedMaxB;                  // [B] floor share
   int* nb = plan_smem + 2 * kBalancedMaxB;                // [B] chunks
   int* first = plan_smem + 3 * kBalancedMaxB;             // [B] first chunk
   const int B = p.B, N = p.n_chunks;
-  for (int i = threadIdx.x; i < B; i += blockDim.x) len[i] = min(max(p.seqlens[i], 1), p.max_seqlen);
+  for (int i = threadIdx.x; i < B; i += blockDim.x) {
+    if constexpr (SEL) {
+      const SeqKeys k = seq_keys<true>(p.sel, p.seqlens, i, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
+      len[i] = k.bad ? 1 : k.L;
+    } else {
+      len[i] = min(max(p.seqlens[i], 1), p.max_seqlen);
+    }
+  }
   __syncthreads();
   long long tot = 0;
   for (int i = 0; i < B; ++i) tot += len[i];
@@ -243,7 +254,7 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t x) {
   return pack_f16x2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
 }
 
-template <int D, bool PAGED, bool FP8>
+template <int D, bool PAGED, bool FP8, bool SEL>
 __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const TcParams p) {
@@ -258,7 +269,7 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
   int c, rt, g, b, chunk;
   size_t item;
   if (p.balanced) {
-    const BalancedItem bi = balanced_item(p, reinterpret_cast<int*>(smem + C::kPlanOff));
+    const BalancedItem bi = balanced_item<SEL, PAGED>(p, reinterpret_cast<int*>(smem + C::kPlanOff));
     c = bi.c;
     rt = 0;
     g = bi.g;
@@ -273,11 +284,13 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
     chunk = p.chunk;
     item = ((size_t)b * p.Hkv + g) * p.max_chunks + c;
   }
-  const int L = p.seqlens[b];
-  // invalid lengths are reported (and their rows made NaN) by the combine kernel
-  if (L < p.T || L > p.max_seqlen || (!PAGED && L > p.capacity) ||
-      (PAGED && (L + kPageTokens - 1) / kPageTokens > p.max_blocks))
+  const SeqKeys sk = seq_keys<SEL>(p.sel, p.seqlens, b, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
+  const int L = sk.L;
+  // invalid lengths: their rows are made NaN by the combine kernel
+  if (sk.bad) {
+    if (SEL && threadIdx.x == 0) atomicOr(p.status, DEV_SEQLEN);
     return;
+  }
   const int tok_begin = c * chunk;
   if (tok_begin >= L) return;   // the combine reads only chunks that start before L
   const int t0 = rt * p.TT;                      // first token of this row tile
@@ -293,6 +306,11 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
     return;
   }
   const int n_tiles = (tok_end - tok_begin + kTok - 1) / kTok;
+  // SEL: no row of the tile sees keys [sinks, dead_end)
+  const int dead_end = SEL && p.causal ? L - p.T + t0 + 1 - p.sel.window : 0;
+  // SEL: what a copy of the 16 selected keys from number vt on starts at -- the logical
+  // block (paged), or the row of the [B * capacity] view
+  auto sel_pos = [&](int vt) { return vt + (vt >= sk.s16 ? sk.gap : 0); };
   const int active_warps = (tile_rows + 31) / 32;
   // FP8 with at most 64 rows: softmax warps 2 and 3 are free and convert the second half
   // of every K (warp 3) and V (warp 2) tile beside the producers
@@ -359,6 +377,31 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // First rows, in the [rows, Hkv, d] view of the cache, of the 16-token blocks of the
+  // tile at key tt, read together (the copies' memory clobbers would otherwise serialise
+  // one table read per block); returns how many blocks hold keys below tok_end.
+  constexpr int kBlocks = kTok / kPageTokens;
+  auto tile_rows16 = [&](int tt, int (&rows)[kBlocks]) {
+    const int nb = min(kBlocks, (tok_end - tt + kPageTokens - 1) / kPageTokens);
+    const int32_t* tab = p.page_table + (size_t)b * p.max_blocks;
+#pragma unroll
+    for (int j = 0; j < kBlocks; ++j) {
+      const int pos = SEL ? sel_pos(tt + j * kPageTokens) : tt + j * kPageTokens;
+      rows[j] = j < nb ? (PAGED ? __ldg(tab + pos / kPageTokens) : b * p.capacity + pos) : 0;
+    }
+    if constexpr (PAGED) {
+#pragma unroll
+      for (int j = 0; j < kBlocks; ++j) {
+        if (j < nb && (rows[j] < 0 || rows[j] >= p.num_blocks)) {
+          atomicOr(p.status, DEV_PAGE_ID);
+          rows[j] = 0;   // keep the byte count; the result is flagged invalid
+        }
+        rows[j] *= kPageTokens;
+      }
+    }
+    return nb;
+  };
+
   if (FP8 && (warp == 7 || warp == 6)) {
     // ------------------------------------------------ FP8 producers and converters
     // Lane 0 copies raw e4m3 tiles into a 2-stage ring; the whole warp converts each
@@ -375,30 +418,20 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
     uint64_t* cfull = &bars[is_k ? T_KCFULL : T_VCFULL];
     uint64_t* cempty = &bars[is_k ? T_KCEMPTY : T_VCEMPTY];
     const uint64_t pol = policy_evict_first();
-    constexpr int kBlocks = kTok / kPageTokens;
     auto copy_tile = [&](int i) {      // lane 0 only
       uint8_t* base = raw_ring + (i % kStages) * C::kRawBytes;
       uint64_t* full = &bars[full0 + i % kStages];
       const int tt = tok_begin + i * kTok;
-      if (!PAGED) {
+      if (!PAGED && !SEL) {
         mbar_arrive_expect_tx(full, C::kRawBytes);
         tma_load_3d(base, map, full, 0, g, b * p.capacity + tt, pol);
       } else {
-        const int nb = min(kBlocks, (tok_end - tt + kPageTokens - 1) / kPageTokens);
-        const int32_t* tab = p.page_table + (size_t)b * p.max_blocks + tt / kPageTokens;
         int ids[kBlocks];
-#pragma unroll
-        for (int j = 0; j < kBlocks; ++j) ids[j] = j < nb ? __ldg(tab + j) : 0;
-#pragma unroll
-        for (int j = 0; j < kBlocks; ++j)
-          if (j < nb && (ids[j] < 0 || ids[j] >= p.num_blocks)) {
-            atomicOr(p.status, DEV_PAGE_ID);
-            ids[j] = 0;   // keep the byte count; the result is flagged invalid
-          }
+        const int nb = tile_rows16(tt, ids);
         mbar_arrive_expect_tx(full, nb * kPageTokens * 128);
 #pragma unroll
         for (int j = 0; j < kBlocks; ++j)
-          if (j < nb) tma_load_3d(base + j * kPageTokens * 128, map, full, 0, g, ids[j] * kPageTokens, pol);
+          if (j < nb) tma_load_3d(base + j * kPageTokens * 128, map, full, 0, g, ids[j], pol);
       }
     };
     int issued = 0;
@@ -491,25 +524,8 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
       int last[kStages];
 #pragma unroll
       for (int s = 0; s < kStages; ++s) last[s] = -1;
-      constexpr int kBlocks = kTok / kPageTokens;
-      // physical blocks of one tile, read together (the copies' memory clobbers
-      // would otherwise serialise one table read per block)
-      auto read_ids = [&](int i, int (&ids)[kBlocks]) {
-        const int tt = tok_begin + i * kTok;
-        const int nb = min(kBlocks, (tok_end - tt + kPageTokens - 1) / kPageTokens);
-        const int32_t* tab = p.page_table + (size_t)b * p.max_blocks + tt / kPageTokens;
-#pragma unroll
-        for (int j = 0; j < kBlocks; ++j) ids[j] = j < nb ? __ldg(tab + j) : 0;
-#pragma unroll
-        for (int j = 0; j < kBlocks; ++j)
-          if (j < nb && (ids[j] < 0 || ids[j] >= p.num_blocks)) {
-            atomicOr(p.status, DEV_PAGE_ID);
-            ids[j] = 0;   // keep the byte count; the result is flagged invalid
-          }
-        return nb;
-      };
       int ids[kBlocks] = {};
-      int nb = PAGED ? read_ids(0, ids) : 0;
+      int nb = PAGED || SEL ? tile_rows16(tok_begin, ids) : 0;
       for (int i = 0; i < n_tiles; ++i) {
         const int ks = i % kStages;
         if (i >= kStages && !tc_wait(&bars[empty0 + ks], ((i / kStages) - 1) & 1, abort_flag, p.status)) break;
@@ -517,7 +533,7 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
         uint8_t* base = ring + ks * C::kTileBytes;
         uint64_t* full = &bars[full0 + ks];
         const int tt = tok_begin + i * kTok;
-        if (!PAGED) {
+        if (!PAGED && !SEL) {
           mbar_arrive_expect_tx(full, C::kTileBytes);
 #pragma unroll
           for (int hh = 0; hh < C::kHalves; ++hh)
@@ -529,10 +545,9 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
             if (j >= nb) break;
 #pragma unroll
             for (int hh = 0; hh < C::kHalves; ++hh)
-              tma_load_3d(base + hh * C::kHalfBytes + j * kPageTokens * 128, map, full, hh * 64, g,
-                          ids[j] * kPageTokens, pol);
+              tma_load_3d(base + hh * C::kHalfBytes + j * kPageTokens * 128, map, full, hh * 64, g, ids[j], pol);
           }
-          if (i + 1 < n_tiles) nb = read_ids(i + 1, ids);
+          if (i + 1 < n_tiles) nb = tile_rows16(tt + kTok, ids);
         }
       }
       // no copy may still be landing in shared memory when the CTA exits
@@ -600,6 +615,20 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
         fence_proxy_async_smem();
         __syncwarp();
       }
+      if constexpr (SEL) {
+        // keys [sinks, dead_end) may hold anything too
+        const int tt = tok_begin + i * kTok;
+        const int z0 = max(p.sel.sinks - tt, 0), z1 = min(dead_end - tt, kTok);
+        if (z0 < z1) {
+          uint8_t* vst = smem + C::kVOff + (FP8 ? 0 : ks) * C::kTileBytes;
+          for (int idx = z0 * 8 + lane; idx < z1 * 8; idx += 32)
+#pragma unroll
+            for (int hh = 0; hh < C::kHalves; ++hh)
+              *reinterpret_cast<uint4*>(vst + hh * C::kHalfBytes + idx * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+      }
       tc_fence_after();
       const uint32_t v_lo = desc_lo(sbase + C::kVOff + (FP8 ? 0 : ks) * C::kTileBytes, C::kHalfBytes);
       const uint32_t d = tmem + C::kOCol, pa = tmem + sb * C::kSCols;
@@ -641,6 +670,14 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
       if (lim < kTok) {
 #pragma unroll
         for (int cc = 0; cc < kTok; ++cc) s[cc] = (cc < lim) ? s[cc] : -INFINITY;
+      }
+      if constexpr (SEL) {
+        // not seen either: keys from `sinks` to the window's first key
+        const int z0 = max(p.sel.sinks - key0, 0), z1 = min(end - p.sel.window - key0, kTok);
+        if (z0 < z1) {
+#pragma unroll
+          for (int cc = 0; cc < kTok; ++cc) s[cc] = (cc >= z0 && cc < z1) ? -INFINITY : s[cc];
+        }
       }
       float mx8[8];
 #pragma unroll
@@ -735,8 +772,8 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
   }
 }
 
-template <int D, bool PAGED, bool FP8>
-cudaError_t run_tc(const DecodeLaunch& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
+template <int D, bool PAGED, bool FP8, bool SEL>
+cudaError_t run_tc_as(const DecodeLaunch& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
   using C = TcCfg<D, FP8>;
   const int G = a.Hq / a.Hkv;
   const int TT = decode_tc_tile_tokens(a.T, G);
@@ -773,8 +810,9 @@ cudaError_t run_tc(const DecodeLaunch& a, const CUtensorMap& tk, const CUtensorM
   p.n_chunks = a.n_chunks;
   p.B = a.B;
   p.plan = a.plan;
+  p.sel = a.sel;
   if (a.balanced && (a.B > kBalancedMaxB || row_tiles != 1 || a.n_chunks < a.B)) return cudaErrorInvalidValue;
-  auto kern = decode_tc_kernel<D, PAGED, FP8>;
+  auto kern = decode_tc_kernel<D, PAGED, FP8, SEL>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   if ((long long)a.max_chunks * row_tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
@@ -782,6 +820,12 @@ cudaError_t run_tc(const DecodeLaunch& a, const CUtensorMap& tk, const CUtensorM
   if (a.balanced) grid = dim3((unsigned)a.n_chunks * a.Hkv);
   kern<<<grid, tc_threads<FP8>(), C::kSmemBytes, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
+}
+
+template <int D, bool PAGED, bool FP8>
+cudaError_t run_tc(const DecodeLaunch& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
+  return a.sel.select ? run_tc_as<D, PAGED, FP8, true>(a, tk, tv, stream)
+                      : run_tc_as<D, PAGED, FP8, false>(a, tk, tv, stream);
 }
 
 }  // namespace

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -50,6 +51,17 @@ int decode_balanced_chunks(int B, int Hkv);
 // wait of the library) and then sets DEV_TIMEOUT (csrc/selftest.cu).
 cudaError_t launch_wait_timeout_selftest(unsigned* status, cudaStream_t stream);
 
+// Which keys of its sequence a decode launch reads (the SEL kernel instances); the
+// default, with select == 0, is all of them (the plain instances).
+struct KeySelect {
+  int select = 0;
+  // query at position p sees keys j <= p with j > p - window or j < sinks
+  int window = kMaxDecodeSeqlen;   // at most that, so that position - window - position stays inside int
+  int sinks = 0;
+  int skip = 0;        // > 0: only the keys from position skip (a multiple of 16) on
+  int fixed_len = 0;   // > 0: every sequence has exactly this many keys (seqlens is not read)
+};
+
 struct DecodeLaunch {
   const void* q;
   const void* k;          // contiguous cache or paged pool
@@ -75,6 +87,12 @@ struct DecodeLaunch {
   int fp8 = 0;                    // k/v hold e4m3 codes with per-KV-head scales
   const float* k_scale = nullptr;  // [Hkv]
   const float* v_scale = nullptr;
+  KeySelect sel;
+  // partials of a shared prefix that the combine merges with the launch's own, chunk c of
+  // KV head g at [g * pre_chunks + c], rows of the whole batch in the order (b, t, head of the group)
+  const float* pre_o = nullptr;    // [Hkv, pre_chunks, B * T * G, d]
+  const float* pre_lse = nullptr;  // [Hkv, pre_chunks, B * T * G]
+  int pre_chunks = 0;
 };
 
 struct PrefillLaunch {
@@ -93,6 +111,7 @@ struct PrefillLaunch {
   const int32_t* page_table = nullptr;  // [B, max_blocks], or nullptr for a contiguous cache
   int capacity = 0, max_blocks = 0, num_blocks = 0;
   int max_seqlen = 0;   // > 0: lengths above it are invalid too (attn_decode's max_seqlen_k)
+  int window = 0, sinks = 0;   // window > 0 (at most kMaxDecodeSeqlen): sliding window with `sinks` first tokens visible (causal)
 };
 
 // attn_decode with at least this many new tokens (bf16 cache, automatic splitting)
@@ -117,9 +136,35 @@ struct AppendLaunch {
   const float* v_scale = nullptr;
 };
 
+// Per-head norm, rotation and write of new tokens (csrc/norm_rope.cu).
+struct NormRopeLaunch {
+  const __nv_bfloat16 *q, *k, *v;           // token rows of Hq, Hkv, Hkv heads (v: cached only)
+  long long q_stride, k_stride, v_stride;   // elements between consecutive tokens
+  __nv_bfloat16* q_out;                     // [B, T, Hq, d]
+  __nv_bfloat16* k_out;                     // [B, T, Hkv, d] when not cached
+  const __nv_bfloat16 *q_weight, *k_weight;   // [d], or nullptr: no norm
+  float eps;
+  const float* rope;                        // [rope_rows, rot]: cosines, then sines
+  int rope_rows, rot, interleaved;
+  const int32_t* pos0;                      // [B] position of token 0, or nullptr: 0
+  int B, T, Hq, Hkv, d;
+  unsigned* status;
+  // cached: K and V go to the cache at the tokens' positions
+  int cached = 0;
+  void *k_cache = nullptr, *v_cache = nullptr;
+  const int32_t* page_table = nullptr;
+  int max_blocks = 0, num_blocks = 0, capacity = 0;
+  int fp8 = 0;
+  const float *k_scale = nullptr, *v_scale = nullptr;
+};
+
 // Tokens per split for attn_decode (host heuristic, deterministic in its inputs).
 // fp8: the call reads an FP8 cache (its kernels want other chunk lengths).
 int decode_chunk_tokens(int B, int T, int G, int Hkv, int max_seqlen, int num_splits, bool fp8);
+
+// Tokens per split of a shared prefix of `prefix` tokens, read by `tokens` query tokens
+// (the whole batch's) of G heads per KV head.
+int prefix_chunk_tokens(int tokens, int G, int Hkv, int prefix, int num_splits, bool fp8);
 
 // Tokens per row tile of the tensor-core decode kernel (G query heads per KV head):
 // as many whole tokens as fit in 128 rows, at most T.
@@ -147,10 +192,14 @@ int encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t dim0, uint64_t d
 // its partials in (ATTN_DECODE_NOALLOC_SCRATCH_BYTES), or nullptr if it cannot be had.
 void* noalloc_scratch();
 
+// split kernel alone (partials), or split and combine
+cudaError_t launch_decode_split(const DecodeLaunch& a, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream);
 // tcgen05 split kernel for more than 16 query rows per KV head (K/V maps with 128-row boxes when contiguous)
 cudaError_t launch_decode_tc(const DecodeLaunch& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream);
 cudaError_t launch_append(const AppendLaunch& a, cudaStream_t stream);
+cudaError_t launch_norm_rope(const NormRopeLaunch& a, cudaStream_t stream);
+cudaError_t launch_rope_table(float* table, int rows, int rot, double theta, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillLaunch& a, cudaStream_t stream);
 // copy n whole blocks (src[i] -> dst[i], device id lists) of both pools
 cudaError_t launch_copy_blocks(void* k, void* v, const int32_t* src, const int32_t* dst, int n, int num_blocks,

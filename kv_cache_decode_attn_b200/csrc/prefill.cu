@@ -40,6 +40,14 @@
 // bytes; paged blocks there are never loaded).  Paged caches load each 128-key
 // tile as eight 16-row boxes, one per physical block of the page table.
 //
+// Sliding window with a few first tokens (WIN instances, causal): the query at
+// position p sees keys j <= p with j > p - window or j < sinks.  Each item numbers
+// the keys its 256 rows can see consecutively, in 16-token blocks: the first
+// tokens' blocks, then the blocks from the first row's window on (the gap between
+// them, whole blocks, is skipped), so an item's work is about window + 256 keys
+// whatever its position.  Every K/V tile is eight 16-row boxes in any layout; masks
+// and limits work on the numbers.
+//
 // Online softmax (running maximum m and denominator l per row, base-2 exponent
 // with the scale folded in): a row's reference maximum is only raised when the
 // tile maximum exceeds it by more than 8 (a factor 256), so O in TMEM is rescaled
@@ -139,10 +147,10 @@ enum KvSource { KV_DENSE = 0, KV_CACHE = 1, KV_PAGED = 2, KV_DENSE_GROUPED = 3 }
 // per form by ptxas's spill report: the dense d = 128 softmax needs 216 registers, the
 // other forms spill less with 208 and 88 for the producers (the cached forms' producers
 // also track the sequence lengths and page-table entries).
-template <int D, int KV>
-constexpr int regs_softmax() { return D == 128 && KV == KV_DENSE ? 216 : 208; }
-template <int D, int KV>
-constexpr int regs_io() { return D == 128 && KV == KV_DENSE ? 72 : 88; }
+template <int D, int KV, bool WIN = false>
+constexpr int regs_softmax() { return D == 128 && KV == KV_DENSE && !WIN ? 216 : 208; }
+template <int D, int KV, bool WIN = false>
+constexpr int regs_io() { return D == 128 && KV == KV_DENSE && !WIN ? 72 : 88; }
 static_assert(2 * 128 * regs_softmax<128, KV_DENSE>() + 128 * regs_io<128, KV_DENSE>() <= 168 * kThreads,
               "register split exceeds the launch");
 static_assert(2 * 128 * regs_softmax<64, KV_PAGED>() + 128 * regs_io<64, KV_PAGED>() <= 168 * kThreads,
@@ -171,6 +179,7 @@ struct PrefillParams {
   const int32_t* page_table;   // [B, max_blocks] (paged)
   int max_keys;                // cache capacity in tokens (contiguous) or max_blocks * 16 (paged)
   int max_blocks, num_blocks;
+  int window, sinks;           // WIN instances
 };
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
@@ -186,6 +195,9 @@ struct Item {
   int qb, h, b, n_kv0, n_load;   // n_kv0: K/V tiles of query tile A; n_load: of tile B (>= n_kv0)
   int L, off;                    // keys of the sequence; query row i sees keys j <= off + i (causal)
   bool bad;                      // invalid length (cached forms): the rows are written as NaN
+  // WIN: L and off count the item's selected keys; number v is position v below s16 and
+  // v + gap from there on
+  int s16, gap;
 };
 
 // Work item w.  Dense with short sequences: heaviest causal query blocks first, then
@@ -196,7 +208,7 @@ struct Item {
 // head, then query blocks heaviest first, then the heads of that K/V head --
 // roughly longest-processing-time first, and every reader of one K/V range runs
 // at about the same time, so that range is read from L2.
-template <int KV>
+template <int KV, bool WIN>
 __device__ __forceinline__ Item item_of(int w, const PrefillParams& p, const int* order) {
   Item it;
   if constexpr (KV == KV_DENSE) {
@@ -214,7 +226,25 @@ __device__ __forceinline__ Item item_of(int w, const PrefillParams& p, const int
     it.qb = p.n_qblocks - 1 - rem2 / p.G;
     it.h = kvh * p.G + rem2 % p.G;
   }
-  if constexpr (kDenseKv<KV>) {
+  it.s16 = it.gap = 0;
+  if constexpr (WIN) {
+    int L = p.N;
+    it.bad = false;
+    if constexpr (!kDenseKv<KV>) {
+      L = __ldg(p.seqlens + it.b);
+      it.bad = L < p.N || L > p.max_keys;
+      if (it.bad) L = p.N;             // a safe stand-in; the host checked p.N <= p.max_keys
+    }
+    it.s16 = (p.sinks + kPageTokens - 1) & ~(kPageTokens - 1);
+    // block of the first key in the window of the item's first row
+    const int w0 = max(0, L - p.N + 2 * it.qb * kBM - p.window + 1) & ~(kPageTokens - 1);
+    it.gap = max(0, w0 - it.s16);
+    it.L = L - it.gap;
+    it.off = it.L - p.N;
+    const int nt = (it.L + kBN - 1) / kBN;
+    it.n_kv0 = min((it.off + 2 * it.qb * kBM + kBM + kBN - 1) / kBN, nt);
+    it.n_load = min((it.off + 2 * it.qb * kBM + 2 * kBM + kBN - 1) / kBN, nt);
+  } else if constexpr (kDenseKv<KV>) {
     it.L = p.N;
     it.off = 0;
     it.bad = false;
@@ -288,7 +318,7 @@ __device__ __forceinline__ void exp_store_half(const float (&s)[kBN], float2 sc,
   }
 }
 
-template <int D, int KV>
+template <int D, int KV, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const PrefillParams p) {
@@ -355,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (warp >= 8) {
-  reg_dealloc<regs_io<D, KV>()>();
+  reg_dealloc<regs_io<D, KV, WIN>()>();
   if (warp == 8 || warp == 10) {
     // ------------------------------------------------------------- TMA producers
     // Warp 8 loads Q per item and the K ring, warp 10 the V ring.  Each ring runs on
@@ -397,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         if (lane == 0) item_slot[it % kItemSlots] = w;
-        itm = item_of<KV>(w, p, order);
+        itm = item_of<KV, WIN>(w, p, order);
         if (lane == 0) w_next = (int)gridDim.x + (int)atomicAdd(p.next_item, 1u);
         w_next = __shfl_sync(0xffffffffu, w_next, 0);
         ++q_loaded;
@@ -410,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_4d(smem + C::kQOff + t * C::kTileBytes + hh * C::kHalfBytes, &tmQ, &bars[B_QFULL], hh * 64,
                           itm.h, (2 * itm.qb + t) * kBM, itm.b, once);
           if (w_next < p.n_items) {                 // warm L2 with the next item's Q
-            const Item nx = item_of<KV>(w_next, p, order);
+            const Item nx = item_of<KV, WIN>(w_next, p, order);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -428,13 +458,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           clean_end = true;
           break;
         }
-        itm = item_of<KV>(wi, p, order);
+        itm = item_of<KV, WIN>(wi, p, order);
       }
       const int kvh = itm.h / p.G;
+      // WIN: position of the first key of this lane's 16-token block of tile t
+      auto block_pos = [&](int t) -> int {
+        const int vt = t * kBN + lane * kPageTokens;
+        return vt + (vt >= itm.s16 ? itm.gap : 0);
+      };
       // paged: this lane's physical block of tile t (lanes >= 8 and blocks past L: none)
       auto read_id = [&](int t) -> int {
         const int nb = min(kBlocks, (itm.L - t * kBN + kPageTokens - 1) / kPageTokens);
-        return lane < nb ? __ldg(p.page_table + (size_t)itm.b * p.max_blocks + t * kBlocks + lane) : -1;
+        const int at = WIN ? block_pos(t) / kPageTokens : t * kBlocks + lane;
+        return lane < nb ? __ldg(p.page_table + (size_t)itm.b * p.max_blocks + at) : -1;
       };
       int id = 0;
       if constexpr (KV == KV_PAGED) id = read_id(0);
@@ -446,7 +482,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         last[s] = g;
         uint8_t* const dst = ring + s * C::kTileBytes;
-        if constexpr (KV != KV_PAGED) {
+        if constexpr (WIN && KV != KV_PAGED) {
+          const int nb = min(kBlocks, (itm.L - t * kBN + kPageTokens - 1) / kPageTokens);
+          if (lane == 0) mbar_arrive_expect_tx(&bars[full0 + s], nb * C::kHalves * kPageTokens * 128);
+          __syncwarp();
+          if (lane < nb) {
+#pragma unroll
+            for (int hh = 0; hh < C::kHalves; ++hh)
+              tma_load_4d(dst + hh * C::kHalfBytes + lane * kPageTokens * 128, map, &bars[full0 + s], hh * 64, kvh,
+                          block_pos(t), itm.b, keep);
+          }
+        } else if constexpr (KV != KV_PAGED) {
           if (lane == 0) {
             mbar_arrive_expect_tx(&bars[full0 + s], C::kTileBytes);
 #pragma unroll
@@ -543,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_or_abort(&bars[B_QFULL], it & 1, abort_flag, p.status)) break;
       const int w = __shfl_sync(0xffffffffu, item_slot[it % kItemSlots], 0);
       if (w < 0) break;                    // no more work
-      const Item itm = item_of<KV>(w, p, order);
+      const Item itm = item_of<KV, WIN>(w, p, order);
       const int n_load = __shfl_sync(0xffffffffu, itm.n_load, 0);
       const int n_kv0 = __shfl_sync(0xffffffffu, itm.n_kv0, 0);
       const int g0 = g;
@@ -560,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool next_k = j + 1 < n_load;
         ok = wait_or_abort(&bars[B_VFULL + st], (gj / kVStages) & 1, abort_flag, p.status);
         if (!ok) break;
-        if constexpr (!kDenseKv<KV>) {
+        if constexpr (!kDenseKv<KV> || WIN) {
           // V rows of keys >= L: any bytes (cache) or never loaded (paged); the PV MMAs
           // would multiply them by p = 0.  Zeroed here, by the warp that consumes the V
           // phases in order, before either PV of the tile is issued.
@@ -568,6 +614,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (valid < kBN) {
             uint8_t* vst = smem + C::kVOff + st * C::kTileBytes;
             for (int idx = max(valid, 0) * 8 + lane; idx < kBN * 8; idx += 32)
+#pragma unroll
+              for (int hh = 0; hh < C::kHalves; ++hh)
+                *reinterpret_cast<uint4*>(vst + hh * C::kHalfBytes + idx * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if constexpr (WIN) {
+          // keys that no row of the item sees (between `sinks` and the first row's window)
+          // may hold anything too
+          const int z0 = max(p.sinks - j * kBN, 0);
+          const int z1 = min(__shfl_sync(0xffffffffu, itm.off + 2 * itm.qb * kBM, 0) + 1 - p.window - j * kBN, kBN);
+          if (z0 < z1) {
+            uint8_t* vst = smem + C::kVOff + st * C::kTileBytes;
+            for (int idx = z0 * 8 + lane; idx < z1 * 8; idx += 32)
 #pragma unroll
               for (int hh = 0; hh < C::kHalves; ++hh)
                 *reinterpret_cast<uint4*>(vst + hh * C::kHalfBytes + idx * 16) = make_uint4(0, 0, 0, 0);
@@ -603,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   } else {
-    reg_alloc<regs_softmax<D, KV>()>();
+    reg_alloc<regs_softmax<D, KV, WIN>()>();
     // -------------------------------------------------- softmax warps 0-7
     const int t = warp >> 2;                            // query tile of this group
     const int row = (warp & 3) * 32 + lane;             // TMEM lane == query row in the tile
@@ -618,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[B_QEMPTY]);        // this warp has read the item
     if (w < 0) break;                                   // no more work
-    const Item itm = item_of<KV>(w, p, order);
+    const Item itm = item_of<KV, WIN>(w, p, order);
     const int q_row = (2 * itm.qb + t) * kBM + row;
     const int nkv = t ? itm.n_load : itm.n_kv0;
     float m = -INFINITY, l = 0.f;
@@ -642,6 +703,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kBN; ++c) s[c] = (c < lim) ? s[c] : -INFINITY;
       }
+      bool gap_masked = false;
+      if constexpr (WIN) {
+        // not seen either: keys from `sinks` to the row's window
+        const int z0 = max(p.sinks - key0, 0), z1 = min(itm.off + q_row + 1 - p.window - key0, kBN);
+        if (z0 < z1) {
+          gap_masked = true;
+#pragma unroll
+          for (int c = 0; c < kBN; ++c) s[c] = (c >= z0 && c < z1) ? -INFINITY : s[c];
+        }
+      }
       float mx8[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) mx8[i] = max3f(s[i], s[i + 8], s[i + 16]);
@@ -658,7 +729,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float alpha = 1.f;
       if (warp_raise) {
         const float m_new = fmaxf(m, mx);
-        alpha = ex2(m - m_new);                                 // 0 when m == -inf
+        // 0 when m == -inf (WIN: the row may have seen no key yet, m_new == -inf too)
+        alpha = ex2(m - (WIN && m_new == -INFINITY ? 0.f : m_new));
         m = m_new;
       }
       const float neg_mu = (m == -INFINITY) ? 0.f : -m;
@@ -682,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       // rows with masked keys (-inf scores) take every exponential on the SFU
       constexpr unsigned kFma = exp_fma_pairs<D>();
-      const bool soft = kFma != 0 && !__any_sync(0xffffffffu, lim < kBN);
+      const bool soft = kFma != 0 && !__any_sync(0xffffffffu, lim < kBN || (WIN && gap_masked));
       if (soft) exp_store_half<0, true, kFma>(s, sc2, nm2, sum2, s_addr);
       else exp_store_half<0, false, kFma>(s, sc2, nm2, sum2, s_addr);
       tc_wait_st();
@@ -788,22 +860,24 @@ cudaError_t queue_slot(unsigned** next, unsigned** done) {
   return cudaSuccess;
 }
 
-template <int D, int KV>
+template <int D, int KV, bool WIN = false>
 cudaError_t run_prefill(const PrefillLaunch& a, cudaStream_t stream) {
   using C = PrefillCfg<D>;
   CUtensorMap tq, tk, tv;
-  // 4-D views {d, heads, rows, B}; box {64, 1, 128, 1} with the 128-byte swizzle
-  auto enc = [&](CUtensorMap* m, const void* base, int heads, int rows) {
+  // 4-D views {d, heads, rows, B}; box {64, 1, rows of one copy, 1} with the 128-byte swizzle
+  constexpr int kKvRows = WIN ? kPageTokens : kBN;
+  auto enc = [&](CUtensorMap* m, const void* base, int heads, int rows, int box_rows) {
     cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)a.B};
     cuuint64_t str[3] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2, (cuuint64_t)rows * heads * D * 2};
-    cuuint32_t box[4] = {64, 1, (cuuint32_t)kBN, 1};
+    cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
     return encode_tmap_nd(m, base, 4, dims, str, box);
   };
-  if (enc(&tq, a.q, a.Hq, a.N)) return cudaErrorInvalidValue;
+  if (enc(&tq, a.q, a.Hq, a.N, kBM)) return cudaErrorInvalidValue;
   if constexpr (kDenseKv<KV>) {
-    if (enc(&tk, a.k, a.Hkv, a.N) || enc(&tv, a.v, a.Hkv, a.N)) return cudaErrorInvalidValue;
+    if (enc(&tk, a.k, a.Hkv, a.N, kKvRows) || enc(&tv, a.v, a.Hkv, a.N, kKvRows)) return cudaErrorInvalidValue;
   } else if constexpr (KV == KV_CACHE) {
-    if (enc(&tk, a.k, a.Hkv, a.capacity) || enc(&tv, a.v, a.Hkv, a.capacity)) return cudaErrorInvalidValue;
+    if (enc(&tk, a.k, a.Hkv, a.capacity, kKvRows) || enc(&tv, a.v, a.Hkv, a.capacity, kKvRows))
+      return cudaErrorInvalidValue;
   } else {
     // pools [num_blocks, 16, Hkv, d] as {d, Hkv, num_blocks * 16}; one 16-row box per block
     const uint64_t rows = (uint64_t)a.num_blocks * kPageTokens;
@@ -833,11 +907,13 @@ cudaError_t run_prefill(const PrefillLaunch& a, cudaStream_t stream) {
   p.page_table = a.page_table;
   p.max_blocks = a.max_blocks;
   p.num_blocks = a.num_blocks;
+  p.window = a.window;
+  p.sinks = a.sinks;
   p.max_keys = KV == KV_PAGED ? a.max_blocks * kPageTokens : (KV == KV_CACHE ? a.capacity : a.N);
   if (!kDenseKv<KV> && a.max_seqlen > 0 && a.max_seqlen < p.max_keys) p.max_keys = a.max_seqlen;
   cudaError_t qe = queue_slot(&p.next_item, &p.done_ctas);
   if (qe != cudaSuccess) return qe;
-  auto kern = prefill_kernel<D, KV>;
+  auto kern = prefill_kernel<D, KV, WIN>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   // the softmax warpgroups' register increase waits until the producer warpgroup's
@@ -845,7 +921,7 @@ cudaError_t run_prefill(const PrefillLaunch& a, cudaStream_t stream) {
   // whose launch register count could not cover the split
   cudaFuncAttributes fa;
   if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-  if (fa.numRegs * kThreads < 2 * 128 * regs_softmax<D, KV>() + 128 * regs_io<D, KV>())
+  if (fa.numRegs * kThreads < 2 * 128 * regs_softmax<D, KV, WIN>() + 128 * regs_io<D, KV, WIN>())
     return cudaErrorInvalidConfiguration;
   // persistent: one CTA per SM (each owns all 512 TMEM columns)
   int dev = 0, sms = 0;
@@ -859,6 +935,14 @@ cudaError_t run_prefill(const PrefillLaunch& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_prefill(const PrefillLaunch& a, cudaStream_t stream) {
+  if (a.window > 0) {
+    if (!a.seqlens)
+      return a.d == 128 ? run_prefill<128, KV_DENSE_GROUPED, true>(a, stream)
+                        : run_prefill<64, KV_DENSE_GROUPED, true>(a, stream);
+    if (!a.page_table)
+      return a.d == 128 ? run_prefill<128, KV_CACHE, true>(a, stream) : run_prefill<64, KV_CACHE, true>(a, stream);
+    return a.d == 128 ? run_prefill<128, KV_PAGED, true>(a, stream) : run_prefill<64, KV_PAGED, true>(a, stream);
+  }
   if (!a.seqlens) {
     const bool grouped = 4.0 * a.N * a.d >= kDenseKvHeadBytes;
     if (a.d == 128) return grouped ? run_prefill<128, KV_DENSE_GROUPED>(a, stream) : run_prefill<128, KV_DENSE>(a, stream);

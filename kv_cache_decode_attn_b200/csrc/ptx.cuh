@@ -19,6 +19,7 @@ enum : unsigned {
   DEV_APPEND_RANGE = 4u,
   DEV_TIMEOUT = 8u,
   DEV_SCALE = 16u,
+  DEV_POSITION = 32u,
 };
 
 // wall-clock limit of one bounded wait, in nanoseconds (%globaltimer), and a

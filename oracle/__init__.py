@@ -39,3 +39,4 @@ from .kv_bytes import (  # noqa: F401
 )
 from . import selfcheck  # noqa: F401
 from . import fp8  # noqa: F401
+from . import serving  # noqa: F401
