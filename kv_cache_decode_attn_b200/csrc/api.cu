@@ -90,11 +90,13 @@ int window_max_keys(int max_seqlen_k, int T, int window, int sinks) {
 struct DecodeLayout {
   int R, chunk, max_chunks;
   int balanced, n_chunks;   // balanced split: chunks over the batch (per KV head)
+  int stream;               // CTAs with even shares of the tiles
   size_t o_bytes, lse_offset, plan_offset, total;
 };
 
+// sel: the windowed and shared-prefix calls' splitting, max_seqlen_k being the longest selected range
 bool decode_layout(int B, int T, int Hq, int Hkv, int d, int max_seqlen_k, int num_splits, bool fp8,
-                   DecodeLayout* out) {
+                   DecodeLayout* out, bool sel = false, int ctas_per_sm = 0) {
   if (B < 1 || T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || max_seqlen_k < 1 || num_splits < 0) return false;
   if (max_seqlen_k > kMaxDecodeSeqlen) return false;
   if (d != 64 && d != 128) return false;
@@ -105,9 +107,14 @@ bool decode_layout(int B, int T, int Hq, int Hkv, int d, int max_seqlen_k, int n
   L.balanced = decode_balanced(B, T, Hq / Hkv, num_splits, fp8) ? 1 : 0;
   L.n_chunks = 0;
   size_t items = (size_t)B * Hkv * L.max_chunks;
+  L.stream = 0;
+  if (sel && num_splits == 0 && !decode_uses_tc(L.R, fp8)) {
+    L.stream = decode_stream_ctas(B, L.R, Hkv, max_seqlen_k, fp8, ctas_per_sm);
+    if (L.stream) items = (size_t)L.stream + (size_t)B * Hkv;
+  }
   if (L.balanced) {
     // every sequence gets at least one chunk of the batch's n_chunks
-    L.n_chunks = decode_balanced_chunks(B, Hkv);
+    L.n_chunks = sel ? decode_balanced_chunks(B, Hkv, 1) : decode_balanced_chunks(B, Hkv);
     L.max_chunks = L.n_chunks - B + 1;   // most chunks one (sequence, KV head) can get
     items = (size_t)L.n_chunks * Hkv;
   }
@@ -250,9 +257,10 @@ int decode_impl(const void* q, const void* k_cache, const void* v_cache, const f
   if (Hq / Hkv > 128) return ATTN_ERR_UNSUPPORTED;                       // one token's heads must fit a row tile
   if (fp8 && d != 128) return ATTN_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
+  if (window >= max_seqlen_k || sinks >= max_seqlen_k) window = 0;   // every key up to the own one: plain decode
   const int max_keys = window > 0 ? window_max_keys(max_seqlen_k, T, window, sinks) : max_seqlen_k;
   DecodeLayout L;
-  if (!decode_layout(B, T, Hq, Hkv, d, max_keys, num_splits, fp8, &L)) return ATTN_ERR_INVALID_ARG;
+  if (!decode_layout(B, T, Hq, Hkv, d, max_keys, num_splits, fp8, &L, window > 0)) return ATTN_ERR_INVALID_ARG;
   if (workspace_bytes < L.total) return ATTN_ERR_WORKSPACE;
   if (static_scratch) {
     // attn_decode_noalloc: the library's own array, looked up only once the request is known to be valid
@@ -287,8 +295,8 @@ int decode_impl(const void* q, const void* k_cache, const void* v_cache, const f
     pa.max_blocks = max_blocks_per_seq;
     pa.num_blocks = num_blocks;
     pa.max_seqlen = max_seqlen_k;
-    pa.window = std::min(window, max_seqlen_k);
-    pa.sinks = std::min(sinks, max_seqlen_k);
+    pa.window = window;
+    pa.sinks = sinks;
     return cuda_status(launch_prefill(pa, static_cast<cudaStream_t>(stream)), name);
   }
   DecodeLaunch a;
@@ -323,9 +331,10 @@ int decode_impl(const void* q, const void* k_cache, const void* v_cache, const f
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   if (window > 0) {
-    a.sel.select = 1;   // the same keys, and no overflow
-    a.sel.window = std::min(window, max_seqlen_k);
-    a.sel.sinks = std::min(sinks, max_seqlen_k);
+    a.sel.select = 1;
+    a.sel.window = window;
+    a.sel.sinks = sinks;
+    a.stream = L.stream;
   }
   return cuda_status(launch_decode(a, static_cast<cudaStream_t>(stream)), name);
 }
@@ -333,7 +342,7 @@ int decode_impl(const void* q, const void* k_cache, const void* v_cache, const f
 // Shared-prefix decode: the launches' parts of the workspace.  The prefix's partials are
 // those of one sequence with B * T query tokens; the own part's follow.
 struct SharedLayout {
-  int pre_chunk, pre_chunks;
+  int pre_chunk, pre_chunks, pre_stream;
   size_t pre_lse_offset, own_offset, total;
   DecodeLayout own;
 };
@@ -346,10 +355,12 @@ bool shared_layout(int B, int T, int Hq, int Hkv, int d, int max_seqlen_k, int p
   const int P = prefix_blocks * kPageTokens;
   if (max_seqlen_k - P < T) return false;
   SharedLayout s;
-  if (!decode_layout(B, T, Hq, Hkv, d, max_seqlen_k - P, num_splits, fp8, &s.own)) return false;
+  if (!decode_layout(B, T, Hq, Hkv, d, max_seqlen_k - P, num_splits, fp8, &s.own, true, 1)) return false;
+  const int R = B * T * (Hq / Hkv);   // the prefix's query rows per KV head
   s.pre_chunk = prefix_chunk_tokens(B * T, Hq / Hkv, Hkv, P, num_splits, fp8);
   s.pre_chunks = (P + s.pre_chunk - 1) / s.pre_chunk;
-  const size_t rows = (size_t)Hkv * s.pre_chunks * B * T * (Hq / Hkv);
+  s.pre_stream = num_splits == 0 && !decode_uses_tc(R, fp8) ? decode_stream_ctas(1, R, Hkv, P, fp8, 1) : 0;
+  const size_t rows = (s.pre_stream ? (size_t)s.pre_stream + Hkv : (size_t)Hkv * s.pre_chunks) * R;
   s.pre_lse_offset = (rows * d * sizeof(float) + 255) & ~size_t(255);
   s.own_offset = (s.pre_lse_offset + rows * sizeof(float) + 255) & ~size_t(255);
   s.total = s.own_offset + s.own.total;
@@ -416,6 +427,8 @@ int shared_impl(const void* q, const void* k_cache, const void* v_cache, const f
   pre.v_scale = v_scale;
   pre.sel.select = 1;
   pre.sel.fixed_len = prefix_blocks * kPageTokens;
+  pre.stream = s.pre_stream;
+  pre.fence = 1;
   // each sequence's own keys, and the merge of both parts
   DecodeLaunch own = pre;
   own.seqlens = seqlens_k;
@@ -435,13 +448,24 @@ int shared_impl(const void* q, const void* k_cache, const void* v_cache, const f
   own.balanced = s.own.balanced;
   own.n_chunks = s.own.n_chunks;
   own.plan = s.own.balanced ? reinterpret_cast<int*>(ws + s.own_offset + s.own.plan_offset) : nullptr;
+  own.stream = s.own.stream;
+  own.fence = 0;
+  own.early = 1;
   own.sel.fixed_len = 0;
   own.sel.skip = prefix_blocks * kPageTokens;
   own.pre_o = pre.part_o;
   own.pre_lse = pre.part_lse;
   own.pre_chunks = s.pre_chunks;
-  const int e = cuda_status(launch_decode_split(pre, static_cast<cudaStream_t>(stream)), name);
-  return e != ATTN_OK ? e : cuda_status(launch_decode(own, static_cast<cudaStream_t>(stream)), name);
+  own.pre_stream = s.pre_stream;
+  own.pre_tiles = prefix_blocks * kPageTokens / kDecodeTile + (prefix_blocks * kPageTokens % kDecodeTile != 0);
+  // The own keys bound by memory and the prefix (many rows) by the tensor cores run side by
+  // side: the own part's CTAs, at most one per SM, start first and let the prefix's in at
+  // once; the prefix's launch ends after the own part's, so the combine waits for both.
+  cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_decode_split(own, st_);
+  if (e == cudaSuccess) e = launch_decode_split(pre, st_);
+  if (e == cudaSuccess) e = launch_decode_combine(own, st_);
+  return cuda_status(e, name);
 }
 
 int prefill_cache_impl(const void* q, const void* k_cache, const void* v_cache, const int32_t* seqlens_k,
@@ -691,7 +715,13 @@ int attn_prefill_cache_window(const void* q, const void* k_cache, const void* v_
 size_t attn_decode_window_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int max_seqlen_k, int window, int sinks,
                                           int num_splits) {
   if (window < 1 || sinks < 0 || T < 1 || max_seqlen_k < 1 || max_seqlen_k > kMaxDecodeSeqlen) return 0;
-  return attn_decode_workspace_bytes(B, T, Hq, Hkv, d, window_max_keys(max_seqlen_k, T, window, sinks), num_splits);
+  if (window >= max_seqlen_k || sinks >= max_seqlen_k)
+    return attn_decode_workspace_bytes(B, T, Hq, Hkv, d, max_seqlen_k, num_splits);
+  const int max_keys = window_max_keys(max_seqlen_k, T, window, sinks);
+  DecodeLayout L, L8;   // enough for either cache type, as attn_decode_workspace_bytes
+  if (!decode_layout(B, T, Hq, Hkv, d, max_keys, num_splits, false, &L, true)) return 0;
+  if (!decode_layout(B, T, Hq, Hkv, d, max_keys, num_splits, true, &L8, true)) return 0;
+  return std::max(L.total, L8.total);
 }
 
 int attn_decode_window(const void* q, const void* k_cache, const void* v_cache, const int32_t* seqlens_k,

@@ -32,6 +32,7 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "internal.h"
@@ -63,6 +64,15 @@ struct DecodeCfg {
   static constexpr int kStatsOffset = kBarOffset + 2 * kStages * 8;
   static constexpr int kSmemBytes = kStatsOffset + MT * 4 * 16 * 2 * 4 + 16 + 1024;  // + alignment slack
   static constexpr int kMinBlocks = (kSmemBytes * 2 <= 227 * 1024) ? 2 : 1;
+  // SEL instances merge the warps of a segment while the ring goes on filling: a buffer of
+  // its own, a quarter of the columns at a time
+  static constexpr int kPasses = 4;
+  static constexpr int kPassCols = D / kPasses;
+  static constexpr int kMergeStride = kPassCols + 4;
+  static constexpr int kMergeOffset = (kSmemBytes - 1024 + 15) / 16 * 16;
+  static constexpr int kSelSmemBytes = kMergeOffset + MT * 4 * 16 * kMergeStride * 4 + 1024;
+  static_assert(kMinBlocks == 1 || 2 * (kSelSmemBytes + (int)sizeof(StreamPlan) + 1024) <= 228 * 1024,
+                "two CTAs per SM");
 };
 
 // bf16 pair (low = lower index) -> f16 pair
@@ -84,29 +94,52 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int c = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
-
-  const SeqKeys sk = seq_keys<SEL>(p.sel, p.seqlens, b, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
-  if (sk.bad) {
-    if (threadIdx.x == 0 && c == 0 && g == 0) atomicOr(p.status, DEV_SEQLEN);
-    return;   // the combine kernel writes NaN rows for this sequence
+  const int c = blockIdx.x;
+  int g = blockIdx.y, b = blockIdx.z;
+  int tok_begin, tok_end, n_tiles;
+  size_t item;
+  SeqKeys sk;
+  const StreamPlan* plan = nullptr;
+  int x = 0, x1 = 0;   // p.stream: this CTA's share of the tiles
+  if constexpr (SEL) {
+    if (p.early) launch_dependents();
+    if (p.fence && c == (p.stream ? p.stream : p.max_chunks)) {
+      if (g == 0 && b == 0) grid_dependency_wait();
+      return;
+    }
   }
-  const int L = sk.L;
-  const int tok_begin = c * p.chunk;
-  if (tok_begin >= L) return;
-  const int tok_end = min(tok_begin + p.chunk, L);
-  const int n_tiles = (tok_end - tok_begin + kDecodeTile - 1) / kDecodeTile;
+  if (SEL && p.stream) {
+    __shared__ StreamPlan plan_smem;
+    stream_plan<PAGED>(p, &plan_smem);
+    plan = &plan_smem;
+    const int total = p.Hkv * plan->first[p.B], n = min(p.stream, total);
+    if (c >= n) return;
+    x = stream_begin(c, n, total);
+    x1 = stream_begin(c + 1, n, total);
+  } else {
+    sk = seq_keys<SEL>(p.sel, p.seqlens, b, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
+    if (sk.bad) {
+      if (threadIdx.x == 0 && c == 0 && g == 0) atomicOr(p.status, DEV_SEQLEN);
+      return;   // the combine kernel writes NaN rows for this sequence
+    }
+    tok_begin = c * p.chunk;
+    if (tok_begin >= sk.L) return;
+    tok_end = min(tok_begin + p.chunk, sk.L);
+    n_tiles = (tok_end - tok_begin + kDecodeTile - 1) / kDecodeTile;
+    item = ((size_t)b * p.Hkv + g) * p.max_chunks + c;
+  }
   float scale_log2 = p.scale_log2, v_scale = 1.f;
+  auto bad_scale = [&](int head) {
+    if constexpr (!FP8) return false;
+    const float ks = __ldg(p.k_scale + head), vs = __ldg(p.v_scale + head);
+    return !(ks > 0.f && ks <= 3.402823466e38f && vs > 0.f && vs <= 3.402823466e38f);
+  };
   if constexpr (FP8) {
-    const float ks = __ldg(p.k_scale + g), vs = __ldg(p.v_scale + g);
-    if (!(ks > 0.f && ks <= 3.402823466e38f && vs > 0.f && vs <= 3.402823466e38f)) {
+    if (!(SEL && p.stream) && bad_scale(g)) {
       if (threadIdx.x == 0 && c == 0) atomicOr(p.status, DEV_SCALE);
-      const size_t item = ((size_t)b * p.Hkv + g) * p.max_chunks + c;
       for (int r = threadIdx.x; r < p.R; r += blockDim.x) p.part_lse[item * p.R + r] = NAN;
       return;   // the whole CTA leaves before any barrier: the scales are uniform across it
     }
-    scale_log2 *= ks;
-    v_scale = vs;
   }
 
   if (threadIdx.x == 0) {
@@ -121,8 +154,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
 
   if (warp == C::kConsumerWarps) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) produce_split_tiles<C, PAGED, SEL>(smem, full, empty, &tmK, &tmV, p, b, g, tok_begin, tok_end,
-                                                     n_tiles, sk, abort_flag);
+    if (lane == 0) {
+      if (SEL && p.stream) produce_stream<C, PAGED>(smem, full, empty, &tmK, &tmV, p, plan, x, x1, bad_scale, abort_flag);
+      else produce_split_tiles<C, PAGED, SEL>(smem, full, empty, &tmK, &tmV, p, b, g, tok_begin, tok_end, n_tiles, sk,
+                                              abort_flag);
+    }
     return;
   }
 
@@ -130,6 +166,31 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
   const int wsub = warp & 3;          // which 16 tokens of each tile
   const int mt = warp >> 2;           // which 16 query rows
   const int gid = lane >> 2, tig = lane & 3;
+
+  int at = 0;   // tiles of the segments before
+  do {
+  if constexpr (SEL) {
+    if (p.stream) {
+      const Segment sg = stream_segment<PAGED>(p, plan, x, x1);
+      b = sg.b;
+      g = sg.g;
+      tok_begin = sg.tok_begin;
+      tok_end = sg.tok_end;
+      n_tiles = sg.n_tiles;
+      item = sg.item;
+      sk = sg.sk;
+      if (FP8 && bad_scale(g)) {
+        if (threadIdx.x == 0) atomicOr(p.status, DEV_SCALE);
+        for (int r = threadIdx.x; r < p.R; r += C::kConsumerWarps * 32) p.part_lse[item * p.R + r] = NAN;
+        continue;   // the scales are uniform across the CTA, and the producer leaves the segment out too
+      }
+    }
+  }
+  const int L = sk.L;
+  if constexpr (FP8) {
+    scale_log2 = p.scale_log2 * __ldg(p.k_scale + g);
+    v_scale = __ldg(p.v_scale + g);
+  }
 
   // Query rows r0 = mt*16 + gid and r1 = r0 + 8; row r is (token t = r / G, head g*G + r % G).
   const int r0 = mt * 16 + gid, r1 = r0 + 8;
@@ -190,8 +251,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
   const int lm = lane >> 3, lr = lane & 7;
 
   for (int i = 0; i < n_tiles; ++i) {
-    const int s = i % C::kStages;
-    if (!mbar_wait(&full[s], (i / C::kStages) & 1)) {
+    const int it = SEL ? at + i : i;
+    const int s = it % C::kStages;
+    if (!mbar_wait(&full[s], (it / C::kStages) & 1)) {
       atomicOr(p.status, DEV_TIMEOUT);
       *reinterpret_cast<volatile int*>(abort_flag) = 1;   // every consumer sees it after the barrier below
       break;
@@ -371,6 +433,94 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
     if (lane == 0) mbar_arrive(&empty[s]);
   }
 
+  if constexpr (SEL) {
+    // ------------------------------------------------ merge the four warps (the ring goes on)
+    constexpr int kC = C::kConsumerWarps * 32;
+    if (consumers_abort<kC>(abort_flag)) {
+      // a wait gave up: this segment and the rest of the share are left as NaN
+      for (;;) {
+        for (int r = threadIdx.x; r < p.R; r += kC) p.part_lse[item * p.R + r] = NAN;
+        if (!p.stream || (x += n_tiles) >= x1) return;
+        const Segment sg = stream_segment<PAGED>(p, plan, x, x1);
+        n_tiles = sg.n_tiles;
+        item = sg.item;
+      }
+    }
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (tig == 0) {
+      float* st = stats + ((mt * 4 + wsub) * 16) * 2;
+      st[gid * 2 + 0] = m0;
+      st[gid * 2 + 1] = l0;
+      st[(gid + 8) * 2 + 0] = m1;
+      st[(gid + 8) * 2 + 1] = l1;
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(kC) : "memory");
+    float M0 = -INFINITY, M1 = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float* sw = stats + ((mt * 4 + w) * 16) * 2;
+      M0 = fmaxf(M0, sw[gid * 2]);
+      M1 = fmaxf(M1, sw[(gid + 8) * 2]);
+    }
+    const float f0 = (m0 == -INFINITY) ? 0.f : ex2(m0 - M0);
+    const float f1 = (m1 == -INFINITY) ? 0.f : ex2(m1 - M1);
+    float* merge = reinterpret_cast<float*>(smem + C::kMergeOffset);
+    float* red = merge + ((mt * 4 + wsub) * 16) * C::kMergeStride;
+    float* out = p.part_o + item * (size_t)p.R * D;
+#pragma unroll
+    for (int ps = 0; ps < C::kPasses; ++ps) {
+      constexpr int kN = D / 8 / C::kPasses;   // 8-column blocks per pass
+#pragma unroll
+      for (int nn = 0; nn < kN; ++nn) {
+        const int n = ps * kN + nn;
+        if constexpr (!FP8) {
+          const int col = nn * 8 + tig * 2;
+          *reinterpret_cast<float2*>(red + gid * C::kMergeStride + col) =
+              make_float2(o_acc[n][0] * f0, o_acc[n][1] * f0);
+          *reinterpret_cast<float2*>(red + (gid + 8) * C::kMergeStride + col) =
+              make_float2(o_acc[n][2] * f1, o_acc[n][3] * f1);
+        } else {
+          const int col = tig * 8 + nn;   // d = 32 tig + n, and + 16 in the next group of four
+          red[gid * C::kMergeStride + col] = o_acc[n][0] * f0;
+          red[gid * C::kMergeStride + col + 4] = o_acc[n][1] * f0;
+          red[(gid + 8) * C::kMergeStride + col] = o_acc[n][2] * f1;
+          red[(gid + 8) * C::kMergeStride + col + 4] = o_acc[n][3] * f1;
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kC) : "memory");
+      constexpr int kVec = C::kPassCols / 4;
+      for (int idx = threadIdx.x; idx < p.R * kVec; idx += kC) {
+        const int r = idx / kVec, v = idx - r * kVec;
+        const int col = FP8 ? 32 * (v >> 1) + 16 * (v & 1) + 4 * ps : ps * C::kPassCols + 4 * v;
+        const int rm = r >> 4, rr = r & 15;
+        float mrow = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mrow = fmaxf(mrow, stats[((rm * 4 + w) * 16 + rr) * 2]);
+        float lsum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float mw = stats[((rm * 4 + w) * 16 + rr) * 2];
+          const float fw = (mw == -INFINITY) ? 0.f : ex2(mw - mrow);
+          lsum += stats[((rm * 4 + w) * 16 + rr) * 2 + 1] * fw;
+          const float4 y = *reinterpret_cast<const float4*>(merge + ((rm * 4 + w) * 16 + rr) * C::kMergeStride + 4 * v);
+          acc.x += y.x;
+          acc.y += y.y;
+          acc.z += y.z;
+          acc.w += y.w;
+        }
+        const float inv = lsum > 0.f ? (FP8 ? v_scale / lsum : 1.f / lsum) : 0.f;
+        *reinterpret_cast<float4*>(out + (size_t)r * D + col) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (ps == 0 && v == 0) p.part_lse[item * p.R + r] = lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY;
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kC) : "memory");   // the buffer is free again
+    }
+    at += n_tiles;
+  } else {
   // -------------------------------------------------- merge the four warps
   launch_dependents();   // the combine kernel may start launching (it waits for this grid)
   // every consumer reached here; the ring is idle (all issued tiles consumed)
@@ -379,7 +529,6 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
   // barrier, so none of them can wait at a later named barrier for one that left
   if (*reinterpret_cast<volatile int*>(abort_flag)) {
     // a wait gave up: leave the partial as NaN so the result is visibly invalid
-    const size_t item = ((size_t)b * p.Hkv + g) * p.max_chunks + c;
     for (int r = threadIdx.x; r < p.R; r += C::kConsumerWarps * 32) p.part_lse[item * p.R + r] = NAN;
     return;
   }
@@ -422,7 +571,6 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
   }
   asm volatile("bar.sync 1, %0;" ::"n"(C::kConsumerWarps * 32) : "memory");
 
-  const size_t item = ((size_t)b * p.Hkv + g) * p.max_chunks + c;
   float* out = p.part_o + item * (size_t)p.R * D;
   constexpr int kVec = D / 4;   // float4 per row
   for (int idx = threadIdx.x; idx < p.R * kVec; idx += C::kConsumerWarps * 32) {
@@ -450,6 +598,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
         make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if (col == 0) p.part_lse[item * p.R + r] = lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY;
   }
+  }
+  } while (SEL && p.stream && (x += n_tiles) < x1);
+  if (SEL && !p.early) launch_dependents();
 }
 
 // kPer consecutive partial-output floats of one lane (2 or 4), as a float4.
@@ -486,7 +637,8 @@ __device__ __forceinline__ void accumulate(float (&acc)[kPer], float w, float4 x
 struct PrefixParts {
   const float* o;
   const float* lse;
-  int chunks, rows;   // rows per chunk: B * T * G
+  int chunks, rows;     // rows per chunk: B * T * G
+  int stream, tiles;    // stream > 0: as SplitParams, over tiles per KV head
 };
 template <int D, int kBatch, bool SEL>
 __global__ void __launch_bounds__(256, kBatch >= 8 ? 2 : 5) decode_combine_kernel(const float* __restrict__ part_o,
@@ -507,11 +659,28 @@ __global__ void __launch_bounds__(256, kBatch >= 8 ? 2 : 5) decode_combine_kerne
   const int g = h / p.G, r = t * p.G + (h - g * p.G);
   bool bad = true;
   int nc = 0, L = 0;
+  int before = 0, total = 0;   // p.stream: tiles (per KV head) of the sequences before b, and of all
+  if constexpr (SEL) {
+    if (p.stream) {
+      const int bb = live ? b : 0;
+      for (int j = lane; j < B; j += 32) {
+        const SeqKeys k = seq_keys<true>(p.sel, seqlens, j, p.T, p.max_seqlen, paged != 0, p.capacity, p.max_blocks);
+        const int tiles = k.bad ? 0 : (k.L + kDecodeTile - 1) / kDecodeTile;
+        total += tiles;
+        if (j < bb) before += tiles;
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+        total += __shfl_xor_sync(0xffffffffu, total, off);
+      }
+    }
+  }
   if (live) {
     const SeqKeys sk = seq_keys<SEL>(p.sel, seqlens, b, p.T, p.max_seqlen, paged != 0, p.capacity, p.max_blocks);
     L = sk.L;
     bad = sk.bad;
-    if (!bad && !p.balanced) nc = (L + p.chunk - 1) / p.chunk;
+    if (!bad && !p.balanced && !p.stream) nc = (L + p.chunk - 1) / p.chunk;
   }
   grid_dependency_wait();   // launched early (programmatic dependent launch): the partials are ready after this
   // chunks of this (b, g): fixed length, or the balanced plan the split kernel wrote
@@ -521,7 +690,26 @@ __global__ void __launch_bounds__(256, kBatch >= 8 ? 2 : 5) decode_combine_kerne
     nc = (L + chunk_b - 1) / chunk_b;
     item0 = (size_t)p.Hkv * first + (size_t)g * n_b;
   }
-  const int npre = SEL && nc > 0 ? pre.chunks : 0;
+  if (SEL && p.stream && live && !bad) {
+    const int tiles = (L + kDecodeTile - 1) / kDecodeTile, x0 = before * p.Hkv + g * tiles;
+    const int n = min(p.stream, total * p.Hkv);
+    const int c0 = stream_cta(x0, n, total * p.Hkv);
+    nc = stream_cta(x0 + tiles - 1, n, total * p.Hkv) - c0 + 1;
+    item0 = (size_t)c0 + (size_t)b * p.Hkv + g;
+  }
+  int npre = 0;
+  size_t pre_item0 = 0;
+  if constexpr (SEL) {
+    if (nc > 0 && pre.o) {
+      npre = pre.chunks;
+      pre_item0 = (size_t)g * pre.chunks;
+      if (pre.stream) {
+        const int total = pre.tiles * p.Hkv, n = min(pre.stream, total), c0 = stream_cta(g * pre.tiles, n, total);
+        npre = stream_cta((g + 1) * pre.tiles - 1, n, total) - c0 + 1;
+        pre_item0 = (size_t)c0 + g;
+      }
+    }
+  }
   nc += npre;
 
   float acc[kPer];
@@ -533,7 +721,7 @@ __global__ void __launch_bounds__(256, kBatch >= 8 ? 2 : 5) decode_combine_kerne
     const float* src0 = part_o + (item0 * p.R + r) * D + lane * kPer;
     const size_t cstride = (size_t)p.R * D;                    // floats between consecutive chunks of this row
     // row of the shared prefix's partials: the whole batch's rows of KV head g, in order
-    const size_t pre0 = SEL ? (size_t)g * pre.chunks * pre.rows + (size_t)b * p.R + r : 0;
+    const size_t pre0 = SEL ? pre_item0 * pre.rows + (size_t)b * p.R + r : 0;
     auto chunk_lse = [&](int c) -> const float* {
       if constexpr (SEL) {
         if (c < npre) return pre.lse + pre0 + (size_t)c * pre.rows;
@@ -652,10 +840,12 @@ cudaError_t run_split_as(const CUtensorMap& tk, const CUtensorMap& tv, const Spl
                       cudaStream_t stream) {
   using C = DecodeCfg<D, MT, FP8>;
   auto kern = decode_split_kernel<D, MT, PAGED, FP8, SEL>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  constexpr int kSmem = SEL ? C::kSelSmemBytes : C::kSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
+  if constexpr (SEL) return launch_sel(kern, C::kThreads, kSmem, tk, tv, sp, B, stream);
   dim3 grid(sp.max_chunks, sp.Hkv, B);
-  kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(tk, tv, sp);
+  kern<<<grid, C::kThreads, kSmem, stream>>>(tk, tv, sp);
   return cudaGetLastError();
 }
 
@@ -693,6 +883,10 @@ SplitParams split_params(const DecodeLaunch& a) {
   sp.balanced = a.balanced;
   sp.plan = a.plan;
   sp.sel = a.sel;
+  sp.B = a.B;
+  sp.stream = a.stream;
+  sp.early = a.early;
+  sp.fence = a.fence;
   return sp;
 }
 
@@ -725,19 +919,37 @@ int decode_chunk_tokens(int B, int T, int G, int Hkv, int max_seqlen, int num_sp
   return chunk < kDecodeTcTile ? kDecodeTcTile : chunk;
 }
 
-int prefix_chunk_tokens(int tokens, int G, int Hkv, int prefix, int num_splits, bool fp8) {
-  return decode_chunk_tokens(1, tokens, G, Hkv, prefix, num_splits, fp8);
-}
-
-int decode_balanced_chunks(int B, int Hkv) {
+namespace {
+int device_sms() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
     cudaGetLastError();   // no device here (workspace sizing on a host without one): a B200's 148 SMs
     sms = 148;
   }
-  const int n = kBalancedItemsPerSlot * kDecodeTcCtasPerSm * sms / Hkv;
+  return sms;
+}
+}  // namespace
+
+int prefix_chunk_tokens(int tokens, int G, int Hkv, int prefix, int num_splits, bool fp8) {
+  if (num_splits > 0 || !decode_uses_tc(G * tokens, fp8))
+    return decode_chunk_tokens(1, tokens, G, Hkv, prefix, num_splits, fp8);
+  const long long units = (long long)Hkv * decode_row_tiles(tokens, G);
+  const long long items = 3LL * device_sms();
+  const long long chunk = std::max((prefix * units + items - 1) / items, 128LL);
+  return (int)((chunk + kDecodeTcTile - 1) / kDecodeTcTile * kDecodeTcTile);
+}
+
+
+int decode_balanced_chunks(int B, int Hkv, int items_per_slot) {
+  const int n = items_per_slot * kDecodeTcCtasPerSm * device_sms() / Hkv;
   return n > B ? n : B;
+}
+
+int decode_stream_ctas(int B, int R, int Hkv, int max_keys, bool fp8, int per_sm) {
+  if (B > kStreamMaxB || (long long)B * Hkv * ((max_keys + kDecodeTile - 1) / kDecodeTile) > INT32_MAX) return 0;
+  if (per_sm == 0) per_sm = fp8 ? (R <= 8 ? 3 : (R <= 16 ? 2 : 1)) : 2;
+  return per_sm * device_sms();
 }
 
 cudaError_t launch_decode_split(const DecodeLaunch& a, cudaStream_t stream) {
@@ -776,15 +988,24 @@ cudaError_t launch_decode_split(const DecodeLaunch& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream) {
-  cudaError_t e = launch_decode_split(a, stream);
-  if (e != cudaSuccess) return e;
+  const cudaError_t e = launch_decode_split(a, stream);
+  return e != cudaSuccess ? e : launch_decode_combine(a, stream);
+}
+
+cudaError_t launch_decode_combine(const DecodeLaunch& a, cudaStream_t stream) {
   const SplitParams sp = split_params(a);
 
   // the combine kernel is launched as a programmatic dependent of the split kernel:
   // it starts launching while the split kernel's last CTAs finish and waits for them
   // warps per output row: enough that each warp merges at most four chunks
   int wpr = 1;
-  const int row_chunks = sp.max_chunks + a.pre_chunks;
+  int row_chunks = sp.max_chunks + a.pre_chunks;
+  if (a.sel.select) {
+    // the chunks that a row has when the batch's sequences are of one length
+    auto share = [](int n, int units) { return (n + units - 1) / units + 1; };
+    row_chunks = sp.stream ? share(sp.stream, a.B * a.Hkv) : (a.balanced ? share(a.n_chunks, a.B) : sp.max_chunks);
+    if (a.pre_o) row_chunks += a.pre_stream ? share(a.pre_stream, a.Hkv) : a.pre_chunks;
+  }
   while (wpr < 8 && wpr * 4 < row_chunks) wpr *= 2;
   const long long rows_out = (long long)a.B * a.T * a.Hq;
   cudaLaunchConfig_t cfg = {};
@@ -799,14 +1020,14 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream) {
   cfg.numAttrs = 1;
   const int paged_i = a.page_table != nullptr ? 1 : 0;
   const bool light = row_chunks <= 2;
-  const PrefixParts pre = {a.pre_o, a.pre_lse, a.pre_chunks, a.B * sp.R};
+  const PrefixParts pre = {a.pre_o, a.pre_lse, a.pre_chunks, a.B * sp.R, a.pre_stream, a.pre_tiles};
   auto pick = [&](auto sel) {
     constexpr bool S = decltype(sel)::value;
     return a.d == 128 ? (light ? decode_combine_kernel<128, 2, S> : decode_combine_kernel<128, 8, S>)
                       : (light ? decode_combine_kernel<64, 2, S> : decode_combine_kernel<64, 8, S>);
   };
   auto kern = a.sel.select ? pick(std::true_type{}) : pick(std::false_type{});
-  e = cudaLaunchKernelEx(&cfg, kern, (const float*)a.part_o, (const float*)a.part_lse, a.seqlens, a.o, a.o_bf16,
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, (const float*)a.part_o, (const float*)a.part_lse, a.seqlens, a.o, a.o_bf16,
                          a.lse, sp, a.B, paged_i, wpr, pre);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

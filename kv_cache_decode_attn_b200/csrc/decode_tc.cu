@@ -131,6 +131,7 @@ struct TcParams {
   int balanced, n_chunks, B;   // balanced split: n_chunks over the batch (per KV head)
   int* plan;                   // [B, 3] written by CTA 0 for the combine kernel
   KeySelect sel;               // SEL instances: which keys of a sequence the launch reads
+  int early = 0, fence = 0;    // SEL instances: as in SplitParams
 };
 
 // Balanced split: the chunks of this launch and this CTA's (sequence, KV head, chunk),
@@ -268,6 +269,13 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int c, rt, g, b, chunk;
   size_t item;
+  if constexpr (SEL) {
+    if (p.early) launch_dependents();
+    if (p.fence && blockIdx.x == gridDim.x - 1) {
+      if (blockIdx.y == 0 && blockIdx.z == 0) grid_dependency_wait();
+      return;
+    }
+  }
   if (p.balanced) {
     const BalancedItem bi = balanced_item<SEL, PAGED>(p, reinterpret_cast<int*>(smem + C::kPlanOff));
     c = bi.c;
@@ -811,6 +819,8 @@ cudaError_t run_tc_as(const DecodeLaunch& a, const CUtensorMap& tk, const CUtens
   p.B = a.B;
   p.plan = a.plan;
   p.sel = a.sel;
+  p.early = a.early;
+  p.fence = a.fence;
   if (a.balanced && (a.B > kBalancedMaxB || row_tiles != 1 || a.n_chunks < a.B)) return cudaErrorInvalidValue;
   auto kern = decode_tc_kernel<D, PAGED, FP8, SEL>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
@@ -818,6 +828,10 @@ cudaError_t run_tc_as(const DecodeLaunch& a, const CUtensorMap& tk, const CUtens
   if ((long long)a.max_chunks * row_tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
   dim3 grid(a.max_chunks * row_tiles, a.Hkv, a.B);
   if (a.balanced) grid = dim3((unsigned)a.n_chunks * a.Hkv);
+  if constexpr (SEL) {
+    grid.x += a.fence;
+    return launch_beside(kern, grid, tc_threads<FP8>(), C::kSmemBytes, stream, a.fence != 0, tq, tk, tv, p);
+  }
   kern<<<grid, tc_threads<FP8>(), C::kSmemBytes, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }

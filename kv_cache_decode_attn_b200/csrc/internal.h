@@ -45,7 +45,12 @@ inline bool decode_balanced(int B, int T, int G, int num_splits, bool fp8) {
   return num_splits == 0 && B <= kBalancedMaxB && decode_uses_tc(G * T, fp8) && G * T <= 128;
 }
 // Chunks over the whole batch (per KV head) of the balanced split on the current device.
-int decode_balanced_chunks(int B, int Hkv);
+int decode_balanced_chunks(int B, int Hkv, int items_per_slot = kBalancedItemsPerSlot);
+
+// Windowed and shared-prefix decode (the SEL instances) on the warp-level kernels, automatic
+// splitting: this many CTAs share the tiles evenly (0: too many sequences or tiles for it,
+// one CTA per chunk then).  per_sm > 0 sets the CTAs per SM, else as many as are resident.
+int decode_stream_ctas(int B, int R, int Hkv, int max_keys, bool fp8, int per_sm = 0);
 
 // One CTA whose thread waits on an mbarrier nothing arrives at (bounded like every
 // wait of the library) and then sets DEV_TIMEOUT (csrc/selftest.cu).
@@ -88,11 +93,15 @@ struct DecodeLaunch {
   const float* k_scale = nullptr;  // [Hkv]
   const float* v_scale = nullptr;
   KeySelect sel;
+  int stream = 0;   // sel, > 0: CTAs that share the tiles evenly; the partials number stream + B * Hkv
+  int early = 0;    // the split kernel lets the next one start at once (one with fence set)
+  int fence = 0;    // the split kernel runs beside the one before, and ends after it
   // partials of a shared prefix that the combine merges with the launch's own, chunk c of
   // KV head g at [g * pre_chunks + c], rows of the whole batch in the order (b, t, head of the group)
   const float* pre_o = nullptr;    // [Hkv, pre_chunks, B * T * G, d]
   const float* pre_lse = nullptr;  // [Hkv, pre_chunks, B * T * G]
   int pre_chunks = 0;
+  int pre_stream = 0, pre_tiles = 0;   // pre_stream > 0: the prefix's pre_tiles tiles per KV head were shared evenly
 };
 
 struct PrefillLaunch {
@@ -192,8 +201,9 @@ int encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t dim0, uint64_t d
 // its partials in (ATTN_DECODE_NOALLOC_SCRATCH_BYTES), or nullptr if it cannot be had.
 void* noalloc_scratch();
 
-// split kernel alone (partials), or split and combine
+// split kernel (partials), combine kernel, or both
 cudaError_t launch_decode_split(const DecodeLaunch& a, cudaStream_t stream);
+cudaError_t launch_decode_combine(const DecodeLaunch& a, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream);
 // tcgen05 split kernel for more than 16 query rows per KV head (K/V maps with 128-row boxes when contiguous)
 cudaError_t launch_decode_tc(const DecodeLaunch& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream);

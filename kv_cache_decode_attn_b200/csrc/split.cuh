@@ -26,6 +26,10 @@ struct SplitParams {
   int balanced = 0;            // tensor-core balanced split: partials indexed by the plan
   const int* plan = nullptr;   // [B, 3]: first chunk, chunks, chunk length per sequence
   KeySelect sel;               // SEL instances: which keys of a sequence the launch reads
+  int B = 0;
+  int stream = 0;              // SEL instances, > 0: CTAs that share the launch's tiles evenly (see StreamPlan)
+  int early = 0;               // SEL instances: let the next kernel start at once; it waits for this one
+  int fence = 0;               // SEL instances: one CTA more, which only waits for the kernel before
 };
 
 __device__ __forceinline__ bool seqlen_bad(int L, int T, int max_seqlen, bool paged, int capacity, int max_blocks) {
@@ -80,27 +84,110 @@ __device__ __forceinline__ SeqKeys seq_keys(const KeySelect& sel, const int32_t*
   return k;
 }
 
+// Even shares (SEL instances, p.stream CTAs).  The launch's 64-token tiles stand in one
+// line, sequence by sequence, the KV heads of a sequence one after the other, and CTA i
+// takes the tiles [i * total / n, (i + 1) * total / n): at most one tile more than any
+// other, whatever the lengths, and the ring runs on across the (sequence, KV head) pairs
+// of a share.  With a fixed chunk length the items came to 2.2 waves of CTAs for a window
+// of 1024 (16 x 8 pairs), and two in five slots idled.  Piece (CTA i, pair u) has partial
+// number i + u: along the line each step raises i or u, so the numbers are distinct, and
+// those of one pair are consecutive.
+constexpr int kStreamMaxB = 256;   // sequences whose tile counts are summed in shared memory
+struct StreamPlan {
+  int first[kStreamMaxB + 1];   // tiles (per KV head) of the sequences before
+  int len[kStreamMaxB];         // keys of the sequences (seqlens)
+};
+
+// First tile of CTA i's share, and the CTA that tile x belongs to.
+__device__ __forceinline__ int stream_begin(int i, int n, int total) { return (int)((long long)i * total / n); }
+__device__ __forceinline__ int stream_cta(int x, int n, int total) {
+  return (int)(((long long)(x + 1) * n + total - 1) / total) - 1;
+}
+
+// All threads of the CTA: tile counts of the sequences, summed (0 for an invalid length,
+// which CTA 0 reports).
+template <bool PAGED>
+__device__ __forceinline__ void stream_plan(const SplitParams& p, StreamPlan* plan) {
+  for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
+    const SeqKeys k = seq_keys<true>(p.sel, p.seqlens, i, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
+    if (k.bad && blockIdx.x == 0) atomicOr(p.status, DEV_SEQLEN);
+    plan->first[i + 1] = k.bad ? 0 : (k.L + kDecodeTile - 1) / kDecodeTile;
+    plan->len[i] = p.sel.fixed_len ? 0 : p.seqlens[i];
+  }
+  if (threadIdx.x == 0) plan->first[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int carry = 0;
+    for (int base = 0; base < p.B; base += 32) {
+      const int i = base + lane;
+      int v = i < p.B ? plan->first[i + 1] : 0;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += u;
+      }
+      v += carry;
+      if (i < p.B) plan->first[i + 1] = v;
+      carry = __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// A run of consecutive tiles of one (sequence, KV head): keys [tok_begin, tok_end), whose
+// partial is number `item`.
+struct Segment {
+  int b, g, tok_begin, tok_end, n_tiles;
+  size_t item;
+  SeqKeys sk;
+};
+
+// The segment that starts at tile x of the line, within the CTA's share [x, x1).
+template <bool PAGED>
+__device__ __forceinline__ Segment stream_segment(const SplitParams& p, const StreamPlan* plan, int x, int x1) {
+  int lo = 0, hi = p.B - 1;   // the last sequence whose first tile is at or before x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.Hkv * plan->first[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  Segment s;
+  s.b = lo;
+  const int tiles = plan->first[lo + 1] - plan->first[lo];
+  const int rem = x - p.Hkv * plan->first[lo];
+  s.g = rem / tiles;
+  const int t0 = rem - s.g * tiles;
+  s.n_tiles = min(tiles - t0, x1 - x);
+  s.sk = seq_keys<true>(p.sel, plan->len, s.b, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
+  s.tok_begin = t0 * kDecodeTile;
+  s.tok_end = min(s.tok_begin + s.n_tiles * kDecodeTile, s.sk.L);
+  s.item = (size_t)blockIdx.x + (size_t)s.b * p.Hkv + s.g;
+  return s;
+}
+
 // One thread: tiles 0 .. n_tiles-1 of keys [tok_begin, tok_end) into the ring of
 // C::kStages stages (K then V, C::kHalves 128-byte swizzle spans per token row;
 // contiguous: one 64-row box per span; paged: one 16-row box per physical
 // block, its page-table entry bounds-checked first; SEL instances: one 16-row box per
-// selected block in either layout), evict-first L2 policy.  A
-// stage is refilled once the consumers released it (empty barrier); a wait that
+// selected block in either layout), evict-first L2 policy.  The ring stands at tile
+// number `at` of the CTA.  A stage is refilled once the consumers released it (empty barrier); a wait that
 // gives up sets DEV_TIMEOUT and the abort flag.
 template <class C, bool PAGED, bool SEL>
-__device__ __forceinline__ void produce_split_tiles(uint8_t* smem, uint64_t* full, uint64_t* empty,
+__device__ __forceinline__ bool produce_split_tiles(uint8_t* smem, uint64_t* full, uint64_t* empty,
                                                     const CUtensorMap* tmK, const CUtensorMap* tmV,
                                                     const SplitParams& p, int b, int g, int tok_begin, int tok_end,
-                                                    int n_tiles, const SeqKeys& sk, int* abort_flag) {
+                                                    int n_tiles, const SeqKeys& sk, int* abort_flag, int at = 0) {
   prefetch_tmap(tmK);
   prefetch_tmap(tmV);
   const uint64_t pol = policy_evict_first();
   for (int i = 0; i < n_tiles; ++i) {
-    const int s = i % C::kStages;
-    if (i >= C::kStages && !mbar_wait(&empty[s], ((i / C::kStages) - 1) & 1)) {
+    const int it = at + i;
+    const int s = it % C::kStages;
+    if (it >= C::kStages && !mbar_wait(&empty[s], ((it / C::kStages) - 1) & 1)) {
       atomicOr(p.status, DEV_TIMEOUT);
       *reinterpret_cast<volatile int*>(abort_flag) = 1;
-      break;
+      return false;
     }
     uint8_t* kst = smem + s * C::kStageBytes;
     uint8_t* vst = kst + C::kTensorBytes;
@@ -149,6 +236,70 @@ __device__ __forceinline__ void produce_split_tiles(uint8_t* smem, uint64_t* ful
       }
     }
   }
+  return true;
+}
+
+// One thread: the tiles of a share [x, x1) of the line, segment after segment.  `skip`
+// tells which KV heads the CTA leaves out (the consumers leave out the same ones).
+template <class C, bool PAGED, class Skip>
+__device__ __forceinline__ void produce_stream(uint8_t* smem, uint64_t* full, uint64_t* empty, const CUtensorMap* tmK,
+                                               const CUtensorMap* tmV, const SplitParams& p, const StreamPlan* plan,
+                                               int x, int x1, Skip skip, int* abort_flag) {
+  int at = 0;
+  while (x < x1) {
+    const Segment s = stream_segment<PAGED>(p, plan, x, x1);
+    if (!skip(s.g)) {
+      if (!produce_split_tiles<C, PAGED, true>(smem, full, empty, tmK, tmV, p, s.b, s.g, s.tok_begin, s.tok_end,
+                                               s.n_tiles, s.sk, abort_flag, at))
+        return;
+      at += s.n_tiles;
+    }
+    x += s.n_tiles;
+  }
+}
+
+// Whether any consumer thread of the CTA (all kThreads of them call this) sees the abort
+// flag: one answer for all, so that none waits at a later barrier for one that left.
+template <int kThreads>
+__device__ __forceinline__ bool consumers_abort(const volatile int* abort_flag) {
+  int r;
+  asm volatile(
+      "{\n"
+      ".reg .pred q, r;\n"
+      "setp.ne.s32 q, %1, 0;\n"
+      "barrier.cta.red.or.pred r, 1, %2, q;\n"
+      "selp.s32 %0, 1, 0, r;\n"
+      "}\n"
+      : "=r"(r)
+      : "r"(*abort_flag), "n"(kThreads)
+      : "memory");
+  return r != 0;
+}
+
+// Launch a kernel; `beside`: without waiting for the one before it in the stream.
+template <class Kernel, class... Args>
+inline cudaError_t launch_beside(Kernel kern, dim3 grid, int threads, int smem, cudaStream_t stream, bool beside,
+                                 const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Launch a SEL instance of a warp-level kernel: p.stream CTAs or one per chunk, one more with p.fence.
+template <class Kernel>
+inline cudaError_t launch_sel(Kernel kern, int threads, int smem, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const SplitParams& sp, int B, cudaStream_t stream) {
+  const dim3 grid = sp.stream ? dim3(sp.stream + sp.fence) : dim3(sp.max_chunks + sp.fence, sp.Hkv, B);
+  return launch_beside(kern, grid, threads, smem, stream, sp.fence != 0, tk, tv, sp);
 }
 
 // FP8 caches, at most 8 query rows per KV head: the transposed-product split kernel (decode_fp8.cu)
