@@ -90,7 +90,7 @@ int window_max_keys(int max_seqlen_k, int T, int window, int sinks) {
 struct DecodeLayout {
   int R, chunk, max_chunks;
   int balanced, n_chunks;   // balanced split: chunks over the batch (per KV head)
-  int stream;               // CTAs with even shares of the tiles
+  int stream;               // CTAs per KV head with even shares of its tiles
   size_t o_bytes, lse_offset, plan_offset, total;
 };
 
@@ -110,7 +110,7 @@ bool decode_layout(int B, int T, int Hq, int Hkv, int d, int max_seqlen_k, int n
   L.stream = 0;
   if (sel && num_splits == 0 && !decode_uses_tc(L.R, fp8)) {
     L.stream = decode_stream_ctas(B, L.R, Hkv, max_seqlen_k, fp8, ctas_per_sm);
-    if (L.stream) items = (size_t)L.stream + (size_t)B * Hkv;
+    if (L.stream) items = ((size_t)L.stream + B) * Hkv;
   }
   if (L.balanced) {
     // every sequence gets at least one chunk of the batch's n_chunks
@@ -360,7 +360,7 @@ bool shared_layout(int B, int T, int Hq, int Hkv, int d, int max_seqlen_k, int p
   s.pre_chunk = prefix_chunk_tokens(B * T, Hq / Hkv, Hkv, P, num_splits, fp8);
   s.pre_chunks = (P + s.pre_chunk - 1) / s.pre_chunk;
   s.pre_stream = num_splits == 0 && !decode_uses_tc(R, fp8) ? decode_stream_ctas(1, R, Hkv, P, fp8, 1) : 0;
-  const size_t rows = (s.pre_stream ? (size_t)s.pre_stream + Hkv : (size_t)Hkv * s.pre_chunks) * R;
+  const size_t rows = (s.pre_stream ? s.pre_stream + 1 : s.pre_chunks) * (size_t)Hkv * R;
   s.pre_lse_offset = (rows * d * sizeof(float) + 255) & ~size_t(255);
   s.own_offset = (s.pre_lse_offset + rows * sizeof(float) + 255) & ~size_t(255);
   s.total = s.own_offset + s.own.total;

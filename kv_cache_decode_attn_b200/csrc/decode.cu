@@ -65,12 +65,11 @@ struct DecodeCfg {
   static constexpr int kSmemBytes = kStatsOffset + MT * 4 * 16 * 2 * 4 + 16 + 1024;  // + alignment slack
   static constexpr int kMinBlocks = (kSmemBytes * 2 <= 227 * 1024) ? 2 : 1;
   // SEL instances merge the warps of a segment while the ring goes on filling: a buffer of
-  // its own, a quarter of the columns at a time
-  static constexpr int kPasses = 4;
-  static constexpr int kPassCols = D / kPasses;
-  static constexpr int kMergeStride = kPassCols + 4;
+  // its own, for four rows of each row group at a time
+  static constexpr int kPassRows = 4;
+  static constexpr int kMergeStride = D + 8;
   static constexpr int kMergeOffset = (kSmemBytes - 1024 + 15) / 16 * 16;
-  static constexpr int kSelSmemBytes = kMergeOffset + MT * 4 * 16 * kMergeStride * 4 + 1024;
+  static constexpr int kSelSmemBytes = kMergeOffset + MT * 4 * kPassRows * kMergeStride * 4 + 1024;
   static_assert(kMinBlocks == 1 || 2 * (kSelSmemBytes + (int)sizeof(StreamPlan) + 1024) <= 228 * 1024,
                 "two CTAs per SM");
 };
@@ -103,19 +102,34 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
   int x = 0, x1 = 0;   // p.stream: this CTA's share of the tiles
   if constexpr (SEL) {
     if (p.early) launch_dependents();
-    if (p.fence && c == (p.stream ? p.stream : p.max_chunks)) {
+    if (p.fence && c == (p.stream ? p.stream * p.Hkv : p.max_chunks)) {
       if (g == 0 && b == 0) grid_dependency_wait();
       return;
     }
   }
+  auto init_ring = [&] {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < C::kStages; ++s) {
+        mbar_init(&full[s], 1);
+        mbar_init(&empty[s], C::kConsumerWarps);
+      }
+      *abort_flag = 0;
+      fence_mbar_init();
+    }
+  };
   if (SEL && p.stream) {
     __shared__ StreamPlan plan_smem;
+    if (threadIdx.x == C::kConsumerWarps * 32) {
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+    }
+    init_ring();
     stream_plan<PAGED>(p, &plan_smem);
     plan = &plan_smem;
-    const int total = p.Hkv * plan->first[p.B], n = min(p.stream, total);
-    if (c >= n) return;
-    x = stream_begin(c, n, total);
-    x1 = stream_begin(c + 1, n, total);
+    const int total = plan->first[p.B], n = min(p.stream, total), i = c / p.Hkv;
+    if (i >= n) return;
+    x = stream_begin(i, n, total);
+    x1 = stream_begin(i + 1, n, total);
   } else {
     sk = seq_keys<SEL>(p.sel, p.seqlens, b, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
     if (sk.bad) {
@@ -142,22 +156,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
     }
   }
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], C::kConsumerWarps);
-    }
-    *abort_flag = 0;
-    fence_mbar_init();
+  if (!(SEL && p.stream)) {   // else done before the plan, whose barriers cover it
+    init_ring();
+    __syncthreads();
   }
-  __syncthreads();
 
   if (warp == C::kConsumerWarps) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      if (SEL && p.stream) produce_stream<C, PAGED>(smem, full, empty, &tmK, &tmV, p, plan, x, x1, bad_scale, abort_flag);
-      else produce_split_tiles<C, PAGED, SEL>(smem, full, empty, &tmK, &tmV, p, b, g, tok_begin, tok_end, n_tiles, sk,
-                                              abort_flag);
+    if (SEL && p.stream) {
+      produce_stream<C, PAGED>(smem, full, empty, &tmK, &tmV, p, plan, x, x1, abort_flag);
+    } else if (lane == 0) {
+      produce_split_tiles<C, PAGED, SEL>(smem, full, empty, &tmK, &tmV, p, b, g, tok_begin, tok_end, n_tiles, sk,
+                                         abort_flag);
     }
     return;
   }
@@ -167,50 +177,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
   const int mt = warp >> 2;           // which 16 query rows
   const int gid = lane >> 2, tig = lane & 3;
 
-  int at = 0;   // tiles of the segments before
-  do {
-  if constexpr (SEL) {
-    if (p.stream) {
-      const Segment sg = stream_segment<PAGED>(p, plan, x, x1);
-      b = sg.b;
-      g = sg.g;
-      tok_begin = sg.tok_begin;
-      tok_end = sg.tok_end;
-      n_tiles = sg.n_tiles;
-      item = sg.item;
-      sk = sg.sk;
-      if (FP8 && bad_scale(g)) {
-        if (threadIdx.x == 0) atomicOr(p.status, DEV_SCALE);
-        for (int r = threadIdx.x; r < p.R; r += C::kConsumerWarps * 32) p.part_lse[item * p.R + r] = NAN;
-        continue;   // the scales are uniform across the CTA, and the producer leaves the segment out too
-      }
-    }
-  }
-  const int L = sk.L;
-  if constexpr (FP8) {
-    scale_log2 = p.scale_log2 * __ldg(p.k_scale + g);
-    v_scale = __ldg(p.v_scale + g);
-  }
-
-  // Query rows r0 = mt*16 + gid and r1 = r0 + 8; row r is (token t = r / G, head g*G + r % G).
-  const int r0 = mt * 16 + gid, r1 = r0 + 8;
-  int end0 = L, end1 = L;   // first invisible key of each row
-  if (p.causal) {
-    if (r0 < p.R) end0 = L - p.T + r0 / p.G + 1;
-    if (r1 < p.R) end1 = L - p.T + r1 / p.G + 1;
-  }
-  // SEL: a row sees keys below `sinks` and from its window's first key on; no row sees
-  // [sinks, dead_end), whose V rows are zeroed like those past L (they may hold anything)
-  const int lo0 = SEL ? end0 - p.sel.window : 0, lo1 = SEL ? end1 - p.sel.window : 0;
-  const int dead_end = SEL && p.causal ? L - p.T + 1 - p.sel.window : 0;
-  auto dead = [&](int tok) { return tok >= L || (SEL && tok >= p.sel.sinks && tok < dead_end); };
-  auto has_dead = [&](int tok0) {   // among tok0 .. tok0 + 15
-    return tok0 + 16 > L || (SEL && tok0 < dead_end && tok0 + 16 > p.sel.sinks);
-  };
-
-  // Q fragments (A operand, 16 x D, row-major) straight from global memory.
+  // Q fragments of a segment (A operand, 16 x D, row-major) straight from global memory.
   uint32_t qa[D / 16][4];
-  {
+  auto load_q = [&](int b, int g) {
+    const int r0 = mt * 16 + gid, r1 = r0 + 8;
     auto qrow = [&](int r) -> const __nv_bfloat16* {
       const int t = r / p.G, hh = r - t * p.G;
       return p.q + (((size_t)b * p.T + t) * p.Hq + (size_t)g * p.G + hh) * D;
@@ -240,7 +210,48 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
         qa[kk][3] = bf16x2_to_f16x2(x1.y);
       }
     }
+  };
+
+  int at = 0;   // tiles of the segments before
+  Segment next;
+  if constexpr (SEL) {
+    if (p.stream) next = stream_segment<PAGED>(p, plan, x, x1);
+    load_q(p.stream ? next.b : b, p.stream ? next.g : g);
   }
+  for (;;) {
+  if constexpr (SEL) {
+    if (p.stream) {
+      b = next.b;
+      g = next.g;
+      tok_begin = next.tok_begin;
+      n_tiles = next.n_tiles;
+      item = next.item;
+      sk = next.sk;
+    }
+  }
+  const int L = sk.L;
+  if constexpr (FP8) {
+    scale_log2 = p.scale_log2 * __ldg(p.k_scale + g);
+    v_scale = __ldg(p.v_scale + g);
+  }
+
+  // Query rows r0 = mt*16 + gid and r1 = r0 + 8; row r is (token t = r / G, head g*G + r % G).
+  const int r0 = mt * 16 + gid, r1 = r0 + 8;
+  int end0 = L, end1 = L;   // first invisible key of each row
+  if (p.causal) {
+    if (r0 < p.R) end0 = L - p.T + r0 / p.G + 1;
+    if (r1 < p.R) end1 = L - p.T + r1 / p.G + 1;
+  }
+  // SEL: a row sees keys below `sinks` and from its window's first key on; no row sees
+  // [sinks, dead_end), whose V rows are zeroed like those past L (they may hold anything)
+  const int lo0 = SEL ? end0 - p.sel.window : 0, lo1 = SEL ? end1 - p.sel.window : 0;
+  const int dead_end = SEL && p.causal ? L - p.T + 1 - p.sel.window : 0;
+  auto dead = [&](int tok) { return tok >= L || (SEL && tok >= p.sel.sinks && tok < dead_end); };
+  auto has_dead = [&](int tok0) {   // among tok0 .. tok0 + 15
+    return tok0 + 16 > L || (SEL && tok0 < dead_end && tok0 + 16 > p.sel.sinks);
+  };
+
+  if constexpr (!SEL) load_q(b, g);
 
   float o_acc[D / 8][4];
 #pragma unroll
@@ -446,6 +457,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
         item = sg.item;
       }
     }
+    at += n_tiles;
+    x += n_tiles;
+    const bool more = p.stream && x < x1;
+    if (more) {   // the next segment's Q is on its way during the merge
+      next = stream_segment<PAGED>(p, plan, x, x1);
+      load_q(next.b, next.g);
+    }
+    bool bad = false;
+    if (FP8 && p.stream && bad_scale(g)) {
+      if (threadIdx.x == 0) atomicOr(p.status, DEV_SCALE);
+      bad = true;
+    }
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
@@ -467,59 +490,57 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
     }
     const float f0 = (m0 == -INFINITY) ? 0.f : ex2(m0 - M0);
     const float f1 = (m1 == -INFINITY) ? 0.f : ex2(m1 - M1);
-    float* merge = reinterpret_cast<float*>(smem + C::kMergeOffset);
-    float* red = merge + ((mt * 4 + wsub) * 16) * C::kMergeStride;
-    float* out = p.part_o + item * (size_t)p.R * D;
+    // pass ps: rows 4 ps .. 4 ps + 3 of each row group; columns stay in fragment order
+    float* merge = reinterpret_cast<float*>(smem + C::kMergeOffset) + mt * 4 * C::kPassRows * C::kMergeStride;
+    const int passes = (min(p.R, 16) + C::kPassRows - 1) / C::kPassRows;
+#pragma unroll 1
+    for (int ps = 0; ps < passes; ++ps) {
+      if (ps > 0) asm volatile("bar.sync 1, %0;" ::"n"(kC) : "memory");   // the buffer has been read
+      if ((gid >> 2) == (ps & 1)) {
+        float* red = merge + (wsub * C::kPassRows + (gid & 3)) * C::kMergeStride + tig * 2;
 #pragma unroll
-    for (int ps = 0; ps < C::kPasses; ++ps) {
-      constexpr int kN = D / 8 / C::kPasses;   // 8-column blocks per pass
-#pragma unroll
-      for (int nn = 0; nn < kN; ++nn) {
-        const int n = ps * kN + nn;
-        if constexpr (!FP8) {
-          const int col = nn * 8 + tig * 2;
-          *reinterpret_cast<float2*>(red + gid * C::kMergeStride + col) =
-              make_float2(o_acc[n][0] * f0, o_acc[n][1] * f0);
-          *reinterpret_cast<float2*>(red + (gid + 8) * C::kMergeStride + col) =
-              make_float2(o_acc[n][2] * f1, o_acc[n][3] * f1);
-        } else {
-          const int col = tig * 8 + nn;   // d = 32 tig + n, and + 16 in the next group of four
-          red[gid * C::kMergeStride + col] = o_acc[n][0] * f0;
-          red[gid * C::kMergeStride + col + 4] = o_acc[n][1] * f0;
-          red[(gid + 8) * C::kMergeStride + col] = o_acc[n][2] * f1;
-          red[(gid + 8) * C::kMergeStride + col + 4] = o_acc[n][3] * f1;
-        }
+        for (int n = 0; n < D / 8; ++n)
+          *reinterpret_cast<float2*>(red + n * 8) = ps < 2 ? make_float2(o_acc[n][0] * f0, o_acc[n][1] * f0)
+                                                           : make_float2(o_acc[n][2] * f1, o_acc[n][3] * f1);
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kC) : "memory");
-      constexpr int kVec = C::kPassCols / 4;
-      for (int idx = threadIdx.x; idx < p.R * kVec; idx += kC) {
-        const int r = idx / kVec, v = idx - r * kVec;
-        const int col = FP8 ? 32 * (v >> 1) + 16 * (v & 1) + 4 * ps : ps * C::kPassCols + 4 * v;
-        const int rm = r >> 4, rr = r & 15;
+      constexpr int kVec = D / 4;
+      const int idx = wsub * 32 + lane, rr = 4 * ps + idx / kVec, r = mt * 16 + rr, v = idx % kVec;
+      if (idx < C::kPassRows * kVec && r < p.R) {
         float mrow = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) mrow = fmaxf(mrow, stats[((rm * 4 + w) * 16 + rr) * 2]);
+        for (int w = 0; w < 4; ++w) mrow = fmaxf(mrow, stats[((mt * 4 + w) * 16 + rr) * 2]);
         float lsum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const float mw = stats[((rm * 4 + w) * 16 + rr) * 2];
+          const float mw = stats[((mt * 4 + w) * 16 + rr) * 2];
           const float fw = (mw == -INFINITY) ? 0.f : ex2(mw - mrow);
-          lsum += stats[((rm * 4 + w) * 16 + rr) * 2 + 1] * fw;
-          const float4 y = *reinterpret_cast<const float4*>(merge + ((rm * 4 + w) * 16 + rr) * C::kMergeStride + 4 * v);
-          acc.x += y.x;
-          acc.y += y.y;
-          acc.z += y.z;
-          acc.w += y.w;
+          lsum += stats[((mt * 4 + w) * 16 + rr) * 2 + 1] * fw;
+          const float* src = merge + (w * C::kPassRows + idx / kVec) * C::kMergeStride;
+          if constexpr (!FP8) {
+            const float4 y = *reinterpret_cast<const float4*>(src + 4 * v);
+            acc.x += y.x;
+            acc.y += y.y;
+            acc.z += y.z;
+            acc.w += y.w;
+          } else {
+            // d = 32 t + n + 16 e stands at 8 n + 2 t + e
+            src += (v & 3) * 32 + (v >> 3) * 2 + ((v >> 2) & 1);
+            acc.x += src[0];
+            acc.y += src[8];
+            acc.z += src[16];
+            acc.w += src[24];
+          }
         }
         const float inv = lsum > 0.f ? (FP8 ? v_scale / lsum : 1.f / lsum) : 0.f;
-        *reinterpret_cast<float4*>(out + (size_t)r * D + col) =
+        *reinterpret_cast<float4*>(p.part_o + (item * p.R + r) * (size_t)D + 4 * v) =
             make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (ps == 0 && v == 0) p.part_lse[item * p.R + r] = lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY;
+        if (v == 0)
+          p.part_lse[item * p.R + r] = bad ? NAN : (lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY);
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(kC) : "memory");   // the buffer is free again
     }
-    at += n_tiles;
+    if (!more) break;
   } else {
   // -------------------------------------------------- merge the four warps
   launch_dependents();   // the combine kernel may start launching (it waits for this grid)
@@ -598,8 +619,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
         make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if (col == 0) p.part_lse[item * p.R + r] = lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY;
   }
+  break;
   }
-  } while (SEL && p.stream && (x += n_tiles) < x1);
+  }
   if (SEL && !p.early) launch_dependents();
 }
 
@@ -638,7 +660,7 @@ struct PrefixParts {
   const float* o;
   const float* lse;
   int chunks, rows;     // rows per chunk: B * T * G
-  int stream, tiles;    // stream > 0: as SplitParams, over tiles per KV head
+  int stream, tiles;    // stream > 0: as in SplitParams, over so many tiles per KV head
 };
 template <int D, int kBatch, bool SEL>
 __global__ void __launch_bounds__(256, kBatch >= 8 ? 2 : 5) decode_combine_kernel(const float* __restrict__ part_o,
@@ -691,11 +713,10 @@ __global__ void __launch_bounds__(256, kBatch >= 8 ? 2 : 5) decode_combine_kerne
     item0 = (size_t)p.Hkv * first + (size_t)g * n_b;
   }
   if (SEL && p.stream && live && !bad) {
-    const int tiles = (L + kDecodeTile - 1) / kDecodeTile, x0 = before * p.Hkv + g * tiles;
-    const int n = min(p.stream, total * p.Hkv);
-    const int c0 = stream_cta(x0, n, total * p.Hkv);
-    nc = stream_cta(x0 + tiles - 1, n, total * p.Hkv) - c0 + 1;
-    item0 = (size_t)c0 + (size_t)b * p.Hkv + g;
+    const int tiles = (L + kDecodeTile - 1) / kDecodeTile, n = min(p.stream, total);
+    const int c0 = stream_cta(before, n, total);
+    nc = stream_cta(before + tiles - 1, n, total) - c0 + 1;
+    item0 = (size_t)g * (p.stream + B) + c0 + b;
   }
   int npre = 0;
   size_t pre_item0 = 0;
@@ -704,9 +725,8 @@ __global__ void __launch_bounds__(256, kBatch >= 8 ? 2 : 5) decode_combine_kerne
       npre = pre.chunks;
       pre_item0 = (size_t)g * pre.chunks;
       if (pre.stream) {
-        const int total = pre.tiles * p.Hkv, n = min(pre.stream, total), c0 = stream_cta(g * pre.tiles, n, total);
-        npre = stream_cta((g + 1) * pre.tiles - 1, n, total) - c0 + 1;
-        pre_item0 = (size_t)c0 + g;
+        npre = min(pre.stream, pre.tiles);
+        pre_item0 = (size_t)g * (pre.stream + 1);
       }
     }
   }
@@ -947,9 +967,9 @@ int decode_balanced_chunks(int B, int Hkv, int items_per_slot) {
 }
 
 int decode_stream_ctas(int B, int R, int Hkv, int max_keys, bool fp8, int per_sm) {
-  if (B > kStreamMaxB || (long long)B * Hkv * ((max_keys + kDecodeTile - 1) / kDecodeTile) > INT32_MAX) return 0;
+  if (B > kStreamMaxB || (long long)B * ((max_keys + kDecodeTile - 1) / kDecodeTile) > INT32_MAX) return 0;
   if (per_sm == 0) per_sm = fp8 ? (R <= 8 ? 3 : (R <= 16 ? 2 : 1)) : 2;
-  return per_sm * device_sms();
+  return std::max(per_sm * device_sms() / Hkv, 1);
 }
 
 cudaError_t launch_decode_split(const DecodeLaunch& a, cudaStream_t stream) {
@@ -972,9 +992,11 @@ cudaError_t launch_decode_split(const DecodeLaunch& a, cudaStream_t stream) {
   cudaError_t e;
   if (tc) {
     e = launch_decode_tc(a, tk, tv, stream);   // bf16 above 16 rows per KV head, FP8 above 32
+  } else if (a.sel.select && R <= 8) {
+    e = launch_decode_rows8(tk, tv, sp, a.B, a.d, a.fp8 != 0, paged, stream);
   } else if (a.fp8) {
     // api.cu admits FP8 caches with d == 128 only
-    if (R <= 8) e = launch_decode_fp8_rows8(tk, tv, sp, a.B, paged, a.sel.select != 0, stream);
+    if (R <= 8) e = launch_decode_fp8_rows8(tk, tv, sp, a.B, paged, stream);
     else if (R <= 16) e = paged ? run_split<128, 1, true, true>(tk, tv, sp, a.B, stream)
                            : run_split<128, 1, false, true>(tk, tv, sp, a.B, stream);
     else e = paged ? run_split<128, 2, true, true>(tk, tv, sp, a.B, stream)
@@ -1003,8 +1025,8 @@ cudaError_t launch_decode_combine(const DecodeLaunch& a, cudaStream_t stream) {
   if (a.sel.select) {
     // the chunks that a row has when the batch's sequences are of one length
     auto share = [](int n, int units) { return (n + units - 1) / units + 1; };
-    row_chunks = sp.stream ? share(sp.stream, a.B * a.Hkv) : (a.balanced ? share(a.n_chunks, a.B) : sp.max_chunks);
-    if (a.pre_o) row_chunks += a.pre_stream ? share(a.pre_stream, a.Hkv) : a.pre_chunks;
+    row_chunks = sp.stream ? share(sp.stream, a.B) : (a.balanced ? share(a.n_chunks, a.B) : sp.max_chunks);
+    if (a.pre_o) row_chunks += a.pre_stream ? std::min(a.pre_stream, a.pre_tiles) : a.pre_chunks;
   }
   while (wpr < 8 && wpr * 4 < row_chunks) wpr *= 2;
   const long long rows_out = (long long)a.B * a.T * a.Hq;

@@ -49,13 +49,6 @@ struct Fp8StCfg {
   static constexpr int kBarOffset = kStages * kStageBytes;
   static constexpr int kStatsOffset = kBarOffset + 2 * kStages * 8;
   static constexpr int kSmemBytes = kStatsOffset + kConsumerWarps * kRows * 2 * 4 + 16 + 1024;
-  // SEL instances merge the warps of a segment while the ring goes on filling: a buffer of
-  // its own, a quarter of the columns at a time
-  static constexpr int kPasses = 4;
-  static constexpr int kMergeStride = 32 + 4;
-  static constexpr int kMergeOffset = (kSmemBytes - 1024 + 15) / 16 * 16;
-  static constexpr int kSelSmemBytes = kMergeOffset + kConsumerWarps * kRows * kMergeStride * 4 + 1024;
-  static_assert(3 * (kSelSmemBytes + (int)sizeof(StreamPlan) + 1024) <= 228 * 1024, "three CTAs per SM");
 };
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
@@ -68,7 +61,7 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
   return pack_f16x2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-template <bool PAGED, bool SEL>
+template <bool PAGED>
 __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
     decode_fp8_st_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const SplitParams p) {
@@ -82,49 +75,25 @@ __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int c = blockIdx.x;
-  int g = blockIdx.y, b = blockIdx.z;
-  int tok_begin, tok_end, n_tiles;
-  size_t item;
-  SeqKeys sk;
-  const StreamPlan* plan = nullptr;
-  int x = 0, x1 = 0;   // p.stream: this CTA's share of the tiles
-  auto bad_scale = [&](int head) {
-    const float ks = __ldg(p.k_scale + head), vs = __ldg(p.v_scale + head);
-    return !(ks > 0.f && ks <= 3.402823466e38f && vs > 0.f && vs <= 3.402823466e38f);
-  };
-  if constexpr (SEL) {
-    if (p.early) launch_dependents();
-    if (p.fence && c == (p.stream ? p.stream : p.max_chunks)) {
-      if (g == 0 && b == 0) grid_dependency_wait();
-      return;
-    }
+  const int c = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
+
+  const int L = p.seqlens[b];
+  if (seqlen_bad(L, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks)) {
+    if (threadIdx.x == 0 && c == 0 && g == 0) atomicOr(p.status, DEV_SEQLEN);
+    return;   // the combine kernel writes NaN rows for this sequence
   }
-  if (SEL && p.stream) {
-    __shared__ StreamPlan plan_smem;
-    stream_plan<PAGED>(p, &plan_smem);
-    plan = &plan_smem;
-    const int total = p.Hkv * plan->first[p.B], n = min(p.stream, total);
-    if (c >= n) return;
-    x = stream_begin(c, n, total);
-    x1 = stream_begin(c + 1, n, total);
-  } else {
-    sk = seq_keys<SEL>(p.sel, p.seqlens, b, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
-    if (sk.bad) {
-      if (threadIdx.x == 0 && c == 0 && g == 0) atomicOr(p.status, DEV_SEQLEN);
-      return;   // the combine kernel writes NaN rows for this sequence
-    }
-    tok_begin = c * p.chunk;
-    if (tok_begin >= sk.L) return;
-    tok_end = min(tok_begin + p.chunk, sk.L);
-    n_tiles = (tok_end - tok_begin + kDecodeTile - 1) / kDecodeTile;
-    item = ((size_t)b * p.Hkv + g) * p.max_chunks + c;
-    if (bad_scale(g)) {
-      if (threadIdx.x == 0 && c == 0) atomicOr(p.status, DEV_SCALE);
-      for (int r = threadIdx.x; r < p.R; r += blockDim.x) p.part_lse[item * p.R + r] = NAN;
-      return;   // the whole CTA leaves before any barrier: the scales are uniform across it
-    }
+  const int tok_begin = c * p.chunk;
+  if (tok_begin >= L) return;
+  const int tok_end = min(tok_begin + p.chunk, L);
+  const int n_tiles = (tok_end - tok_begin + kDecodeTile - 1) / kDecodeTile;
+  const size_t item = ((size_t)b * p.Hkv + g) * p.max_chunks + c;
+  const float ks = __ldg(p.k_scale + g), vs = __ldg(p.v_scale + g);
+  if (!(ks > 0.f && ks <= 3.402823466e38f && vs > 0.f && vs <= 3.402823466e38f)) {
+    if (threadIdx.x == 0 && c == 0) atomicOr(p.status, DEV_SCALE);
+    for (int r = threadIdx.x; r < p.R; r += blockDim.x) p.part_lse[item * p.R + r] = NAN;
+    return;   // the whole CTA leaves before any barrier: the scales are uniform across it
   }
+  const float scale_log2 = p.scale_log2 * ks;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -137,39 +106,14 @@ __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
   __syncthreads();
 
   if (warp == C::kConsumerWarps) {
-    if (lane == 0) {
-      if (SEL && p.stream) produce_stream<C, PAGED>(smem, full, empty, &tmK, &tmV, p, plan, x, x1, bad_scale, abort_flag);
-      else produce_split_tiles<C, PAGED, SEL>(smem, full, empty, &tmK, &tmV, p, b, g, tok_begin, tok_end, n_tiles, sk,
-                                              abort_flag);
-    }
+    if (lane == 0) produce_split_tiles<C, PAGED, false>(smem, full, empty, &tmK, &tmV, p, b, g, tok_begin, tok_end,
+                                                       n_tiles, SeqKeys{}, abort_flag);
     return;
   }
 
   // -------------------------------------------------------------- consumers
   const int wsub = warp;                       // which 16 tokens of each tile
   const int gid = lane >> 2, tig = lane & 3;
-
-  int at = 0;   // tiles of the segments before
-  do {
-  if constexpr (SEL) {
-    if (p.stream) {
-      const Segment sg = stream_segment<PAGED>(p, plan, x, x1);
-      b = sg.b;
-      g = sg.g;
-      tok_begin = sg.tok_begin;
-      tok_end = sg.tok_end;
-      n_tiles = sg.n_tiles;
-      item = sg.item;
-      sk = sg.sk;
-      if (bad_scale(g)) {
-        if (threadIdx.x == 0) atomicOr(p.status, DEV_SCALE);
-        for (int r = threadIdx.x; r < p.R; r += C::kConsumerWarps * 32) p.part_lse[item * p.R + r] = NAN;
-        continue;   // the scales are uniform across the CTA, and the producer leaves the segment out too
-      }
-    }
-  }
-  const int L = sk.L;
-  const float scale_log2 = p.scale_log2 * __ldg(p.k_scale + g), vs = __ldg(p.v_scale + g);
 
   // Q^T (B operand, n = query row gid): k16 step kk takes d = 16 (tig + 4 (kk / 4)) + 4 (kk % 4) + {0, 1 | 2, 3}
   uint32_t qb[8][2];
@@ -190,24 +134,14 @@ __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
   const int end0 = r0 < p.R ? (p.causal ? L - p.T + r0 / p.G + 1 : L) : 0;
   const int end1 = r1 < p.R ? (p.causal ? L - p.T + r1 / p.G + 1 : L) : 0;
 
-  // SEL: a row sees keys below `sinks` and from its window's first key on; no row sees
-  // [sinks, dead_end), whose V rows are zeroed like those past L (they may hold anything)
-  const int lo0 = SEL ? end0 - p.sel.window : 0, lo1 = SEL ? end1 - p.sel.window : 0;
-  const int dead_end = SEL && p.causal ? L - p.T + 1 - p.sel.window : 0;
-  auto dead = [&](int tok) { return tok >= L || (SEL && tok >= p.sel.sinks && tok < dead_end); };
-  auto seen = [&](int tok, int end, int lo) {
-    return tok < end && (!SEL || tok >= lo || tok < p.sel.sinks);
-  };
-
   float o[8][4];
 #pragma unroll
   for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
   for (int i = 0; i < n_tiles; ++i) {
-    const int it = SEL ? at + i : i;
-    const int s = it % C::kStages;
-    if (!mbar_wait(&full[s], (it / C::kStages) & 1)) {
+    const int s = i % C::kStages;
+    if (!mbar_wait(&full[s], (i / C::kStages) & 1)) {
       atomicOr(p.status, DEV_TIMEOUT);
       *reinterpret_cast<volatile int*>(abort_flag) = 1;   // every consumer sees it after the barrier below
       break;
@@ -244,13 +178,13 @@ __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
     //      softmax; keys at or past L may hold any bytes, so their rows are zeroed
     uint32_t vw[4][4];
     {
-      const bool tail = tok_base + 16 > L || (SEL && tok_base < dead_end && tok_base + 16 > p.sel.sinks);
+      const bool tail = tok_base + 16 > L;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int key = 2 * tig + (q & 1) + 8 * (q >> 1);
         const int vrow = wsub * 16 + key;
         uint4 x = lds128(vbase + vrow * 128 + ((gid ^ (vrow & 7)) << 4));
-        if (tail && dead(tok_base + key)) x = make_uint4(0u, 0u, 0u, 0u);
+        if (tail && tok_base + key >= L) x = make_uint4(0u, 0u, 0u, 0u);
         vw[q][0] = x.x;
         vw[q][1] = x.y;
         vw[q][2] = x.z;
@@ -260,10 +194,10 @@ __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
 
     // ---- online softmax over this warp's keys for query rows r0, r1 (base 2, lazy rescale)
     const int ka = tok_base + gid, kb = ka + 8;
-    const float v00 = seen(ka, end0, lo0) ? sacc[0] * scale_log2 : -INFINITY;   // key gid,     row r0
-    const float v01 = seen(ka, end1, lo1) ? sacc[1] * scale_log2 : -INFINITY;   // key gid,     row r1
-    const float v10 = seen(kb, end0, lo0) ? sacc[2] * scale_log2 : -INFINITY;   // key gid + 8, row r0
-    const float v11 = seen(kb, end1, lo1) ? sacc[3] * scale_log2 : -INFINITY;   // key gid + 8, row r1
+    const float v00 = (ka < end0) ? sacc[0] * scale_log2 : -INFINITY;   // key gid,     row r0
+    const float v01 = (ka < end1) ? sacc[1] * scale_log2 : -INFINITY;   // key gid,     row r1
+    const float v10 = (kb < end0) ? sacc[2] * scale_log2 : -INFINITY;   // key gid + 8, row r0
+    const float v11 = (kb < end1) ? sacc[3] * scale_log2 : -INFINITY;   // key gid + 8, row r1
     float mx0 = fmaxf(v00, v10), mx1 = fmaxf(v01, v11);
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
@@ -311,79 +245,6 @@ __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
     if (lane == 0) mbar_arrive(&empty[s]);
   }
 
-  if constexpr (SEL) {
-    // ------------------------------------------------ merge the four warps (the ring goes on)
-    constexpr int kC = C::kConsumerWarps * 32;
-    if (consumers_abort<kC>(abort_flag)) {
-      // a wait gave up: this segment and the rest of the share are left as NaN
-      for (;;) {
-        for (int r = threadIdx.x; r < p.R; r += kC) p.part_lse[item * p.R + r] = NAN;
-        if (!p.stream || (x += n_tiles) >= x1) return;
-        const Segment sg = stream_segment<PAGED>(p, plan, x, x1);
-        n_tiles = sg.n_tiles;
-        item = sg.item;
-      }
-    }
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, off);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, off);
-    }
-    if (gid == 0) {
-      float* st = stats + wsub * C::kRows * 2;
-      st[r0 * 2 + 0] = m0;
-      st[r0 * 2 + 1] = l0;
-      st[r1 * 2 + 0] = m1;
-      st[r1 * 2 + 1] = l1;
-    }
-    asm volatile("bar.sync 1, %0;" ::"n"(kC) : "memory");
-    float M0 = -INFINITY, M1 = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < C::kConsumerWarps; ++w) {
-      M0 = fmaxf(M0, stats[(w * C::kRows + r0) * 2]);
-      M1 = fmaxf(M1, stats[(w * C::kRows + r1) * 2]);
-    }
-    const float f0 = (m0 == -INFINITY) ? 0.f : ex2(m0 - M0);
-    const float f1 = (m1 == -INFINITY) ? 0.f : ex2(m1 - M1);
-    float* merge = reinterpret_cast<float*>(smem + C::kMergeOffset);
-    float* red = merge + wsub * C::kRows * C::kMergeStride;
-    float* out = p.part_o + item * (size_t)p.R * 128;
-#pragma unroll
-    for (int ps = 0; ps < C::kPasses; ++ps) {
-#pragma unroll
-      for (int jj = 0; jj < 2; ++jj) {
-        const int j = 2 * ps + jj, col = 4 * gid + 2 * jj;   // d = 16 gid + 2 j
-        *reinterpret_cast<float2*>(red + r0 * C::kMergeStride + col) = make_float2(o[j][0] * f0, o[j][2] * f0);
-        *reinterpret_cast<float2*>(red + r1 * C::kMergeStride + col) = make_float2(o[j][1] * f1, o[j][3] * f1);
-      }
-      asm volatile("bar.sync 1, %0;" ::"n"(kC) : "memory");
-      for (int idx = threadIdx.x; idx < p.R * 8; idx += kC) {
-        const int r = idx >> 3, v = idx & 7;
-        float mrow = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < C::kConsumerWarps; ++w) mrow = fmaxf(mrow, stats[(w * C::kRows + r) * 2]);
-        float lsum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < C::kConsumerWarps; ++w) {
-          const float mw = stats[(w * C::kRows + r) * 2];
-          const float fw = (mw == -INFINITY) ? 0.f : ex2(mw - mrow);
-          lsum += stats[(w * C::kRows + r) * 2 + 1] * fw;
-          const float4 y = *reinterpret_cast<const float4*>(merge + (w * C::kRows + r) * C::kMergeStride + 4 * v);
-          acc.x += y.x;
-          acc.y += y.y;
-          acc.z += y.z;
-          acc.w += y.w;
-        }
-        const float inv = lsum > 0.f ? vs / lsum : 0.f;
-        *reinterpret_cast<float4*>(out + (size_t)r * 128 + 16 * v + 4 * ps) =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (ps == 0 && v == 0) p.part_lse[item * p.R + r] = lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY;
-      }
-      asm volatile("bar.sync 1, %0;" ::"n"(kC) : "memory");   // the buffer is free again
-    }
-    at += n_tiles;
-  } else {
   // -------------------------------------------------- merge the four warps
   launch_dependents();   // the combine kernel may start launching (it waits for this grid)
   asm volatile("bar.sync 1, %0;" ::"n"(C::kConsumerWarps * 32) : "memory");
@@ -448,29 +309,23 @@ __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
         make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if (col == 0) p.part_lse[item * p.R + r] = lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY;
   }
-  }
-  } while (SEL && p.stream && (x += n_tiles) < x1);
-  if (SEL && !p.early) launch_dependents();
 }
 
-template <bool PAGED, bool SEL>
+template <bool PAGED>
 cudaError_t run(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int B, cudaStream_t stream) {
-  auto kern = decode_fp8_st_kernel<PAGED, SEL>;
-  constexpr int kSmem = SEL ? Fp8StCfg::kSelSmemBytes : Fp8StCfg::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  auto kern = decode_fp8_st_kernel<PAGED>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Fp8StCfg::kSmemBytes);
   if (e != cudaSuccess) return e;
-  if constexpr (SEL) return launch_sel(kern, Fp8StCfg::kThreads, kSmem, tk, tv, sp, B, stream);
   dim3 grid(sp.max_chunks, sp.Hkv, B);
-  kern<<<grid, Fp8StCfg::kThreads, kSmem, stream>>>(tk, tv, sp);
+  kern<<<grid, Fp8StCfg::kThreads, Fp8StCfg::kSmemBytes, stream>>>(tk, tv, sp);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_decode_fp8_rows8(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int B,
-                                    bool paged, bool sel, cudaStream_t stream) {
-  if (sel) return paged ? run<true, true>(tk, tv, sp, B, stream) : run<false, true>(tk, tv, sp, B, stream);
-  return paged ? run<true, false>(tk, tv, sp, B, stream) : run<false, false>(tk, tv, sp, B, stream);
+                                    bool paged, cudaStream_t stream) {
+  return paged ? run<true>(tk, tv, sp, B, stream) : run<false>(tk, tv, sp, B, stream);
 }
 
 }  // namespace kvattn

@@ -48,7 +48,7 @@ inline bool decode_balanced(int B, int T, int G, int num_splits, bool fp8) {
 int decode_balanced_chunks(int B, int Hkv, int items_per_slot = kBalancedItemsPerSlot);
 
 // Windowed and shared-prefix decode (the SEL instances) on the warp-level kernels, automatic
-// splitting: this many CTAs share the tiles evenly (0: too many sequences or tiles for it,
+// splitting: this many CTAs per KV head share its tiles evenly (0: too many sequences or tiles for it,
 // one CTA per chunk then).  per_sm > 0 sets the CTAs per SM, else as many as are resident.
 int decode_stream_ctas(int B, int R, int Hkv, int max_keys, bool fp8, int per_sm = 0);
 
@@ -93,7 +93,7 @@ struct DecodeLaunch {
   const float* k_scale = nullptr;  // [Hkv]
   const float* v_scale = nullptr;
   KeySelect sel;
-  int stream = 0;   // sel, > 0: CTAs that share the tiles evenly; the partials number stream + B * Hkv
+  int stream = 0;   // sel, > 0: CTAs per KV head that share its tiles evenly; stream + B partials per KV head
   int early = 0;    // the split kernel lets the next one start at once (one with fence set)
   int fence = 0;    // the split kernel runs beside the one before, and ends after it
   // partials of a shared prefix that the combine merges with the launch's own, chunk c of

@@ -1,4 +1,5 @@
-// Pieces shared by the split-KV decode kernels (decode.cu, decode_fp8.cu): the
+// Pieces shared by the split-KV decode kernels (decode.cu, decode_fp8.cu,
+// decode_rows8.cu): the
 // launch parameters, the length check, the selection of keys, and the TMA producer
 // loop that streams a work item's 64-token K/V tiles into a shared-memory ring.
 #pragma once
@@ -27,7 +28,7 @@ struct SplitParams {
   const int* plan = nullptr;   // [B, 3]: first chunk, chunks, chunk length per sequence
   KeySelect sel;               // SEL instances: which keys of a sequence the launch reads
   int B = 0;
-  int stream = 0;              // SEL instances, > 0: CTAs that share the launch's tiles evenly (see StreamPlan)
+  int stream = 0;              // SEL instances, > 0: CTAs per KV head that share its tiles evenly (see StreamPlan)
   int early = 0;               // SEL instances: let the next kernel start at once; it waits for this one
   int fence = 0;               // SEL instances: one CTA more, which only waits for the kernel before
 };
@@ -84,24 +85,28 @@ __device__ __forceinline__ SeqKeys seq_keys(const KeySelect& sel, const int32_t*
   return k;
 }
 
-// Even shares (SEL instances, p.stream CTAs).  The launch's 64-token tiles stand in one
-// line, sequence by sequence, the KV heads of a sequence one after the other, and CTA i
-// takes the tiles [i * total / n, (i + 1) * total / n): at most one tile more than any
-// other, whatever the lengths, and the ring runs on across the (sequence, KV head) pairs
-// of a share.  With a fixed chunk length the items came to 2.2 waves of CTAs for a window
-// of 1024 (16 x 8 pairs), and two in five slots idled.  Piece (CTA i, pair u) has partial
-// number i + u: along the line each step raises i or u, so the numbers are distinct, and
-// those of one pair are consecutive.
-constexpr int kStreamMaxB = 256;   // sequences whose tile counts are summed in shared memory
+// Even shares (SEL instances, p.stream CTAs per KV head).  For each KV head the launch's
+// 64-token tiles stand in one line, sequence after sequence, and CTA i of the head's n
+// takes total / n consecutive tiles, the first total % n CTAs one more: even shares
+// whatever the lengths, and the ring runs on across the sequences of a share.  With a fixed
+// chunk length the items came to 2.2 waves of CTAs for a window of 1024 (16 x 8 pairs), and
+// two in five slots idled.  Block c is CTA c / Hkv of head c % Hkv: the heads of a token,
+// which lie side by side in the cache, are read at about the same time.  Piece (CTA i of
+// head g, sequence b) has partial number g * (n + B) + i + b: along a line each step raises
+// i or b, so the numbers are distinct, and those of one sequence are consecutive.
+constexpr int kStreamMaxB = 128;   // sequences whose tile counts are summed in shared memory
 struct StreamPlan {
   int first[kStreamMaxB + 1];   // tiles (per KV head) of the sequences before
   int len[kStreamMaxB];         // keys of the sequences (seqlens)
 };
 
 // First tile of CTA i's share, and the CTA that tile x belongs to.
-__device__ __forceinline__ int stream_begin(int i, int n, int total) { return (int)((long long)i * total / n); }
+__device__ __forceinline__ int stream_begin(int i, int n, int total) {
+  return i * (total / n) + min(i, total % n);
+}
 __device__ __forceinline__ int stream_cta(int x, int n, int total) {
-  return (int)(((long long)(x + 1) * n + total - 1) / total) - 1;
+  const int share = total / n, wide = total % n * (share + 1);   // tiles of the CTAs with one more
+  return x < wide ? x / (share + 1) : (x - total % n) / share;
 }
 
 // All threads of the CTA: tile counts of the sequences, summed (0 for an invalid length,
@@ -143,26 +148,24 @@ struct Segment {
   SeqKeys sk;
 };
 
-// The segment that starts at tile x of the line, within the CTA's share [x, x1).
+// The segment that starts at tile x of the CTA's line, within its share [x, x1).
 template <bool PAGED>
 __device__ __forceinline__ Segment stream_segment(const SplitParams& p, const StreamPlan* plan, int x, int x1) {
   int lo = 0, hi = p.B - 1;   // the last sequence whose first tile is at or before x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (p.Hkv * plan->first[mid] <= x) lo = mid;
+    if (plan->first[mid] <= x) lo = mid;
     else hi = mid - 1;
   }
   Segment s;
   s.b = lo;
-  const int tiles = plan->first[lo + 1] - plan->first[lo];
-  const int rem = x - p.Hkv * plan->first[lo];
-  s.g = rem / tiles;
-  const int t0 = rem - s.g * tiles;
-  s.n_tiles = min(tiles - t0, x1 - x);
+  s.g = blockIdx.x % p.Hkv;
+  const int t0 = x - plan->first[lo];
+  s.n_tiles = min(plan->first[lo + 1] - x, x1 - x);
   s.sk = seq_keys<true>(p.sel, plan->len, s.b, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
   s.tok_begin = t0 * kDecodeTile;
   s.tok_end = min(s.tok_begin + s.n_tiles * kDecodeTile, s.sk.L);
-  s.item = (size_t)blockIdx.x + (size_t)s.b * p.Hkv + s.g;
+  s.item = (size_t)s.g * (p.stream + p.B) + blockIdx.x / p.Hkv + s.b;
   return s;
 }
 
@@ -170,24 +173,23 @@ __device__ __forceinline__ Segment stream_segment(const SplitParams& p, const St
 // C::kStages stages (K then V, C::kHalves 128-byte swizzle spans per token row;
 // contiguous: one 64-row box per span; paged: one 16-row box per physical
 // block, its page-table entry bounds-checked first; SEL instances: one 16-row box per
-// selected block in either layout), evict-first L2 policy.  The ring stands at tile
-// number `at` of the CTA.  A stage is refilled once the consumers released it (empty barrier); a wait that
+// selected block in either layout), evict-first L2 policy.  A
+// stage is refilled once the consumers released it (empty barrier); a wait that
 // gives up sets DEV_TIMEOUT and the abort flag.
 template <class C, bool PAGED, bool SEL>
-__device__ __forceinline__ bool produce_split_tiles(uint8_t* smem, uint64_t* full, uint64_t* empty,
+__device__ __forceinline__ void produce_split_tiles(uint8_t* smem, uint64_t* full, uint64_t* empty,
                                                     const CUtensorMap* tmK, const CUtensorMap* tmV,
                                                     const SplitParams& p, int b, int g, int tok_begin, int tok_end,
-                                                    int n_tiles, const SeqKeys& sk, int* abort_flag, int at = 0) {
+                                                    int n_tiles, const SeqKeys& sk, int* abort_flag) {
   prefetch_tmap(tmK);
   prefetch_tmap(tmV);
   const uint64_t pol = policy_evict_first();
   for (int i = 0; i < n_tiles; ++i) {
-    const int it = at + i;
-    const int s = it % C::kStages;
-    if (it >= C::kStages && !mbar_wait(&empty[s], ((it / C::kStages) - 1) & 1)) {
+    const int s = i % C::kStages;
+    if (i >= C::kStages && !mbar_wait(&empty[s], ((i / C::kStages) - 1) & 1)) {
       atomicOr(p.status, DEV_TIMEOUT);
       *reinterpret_cast<volatile int*>(abort_flag) = 1;
-      return false;
+      break;
     }
     uint8_t* kst = smem + s * C::kStageBytes;
     uint8_t* vst = kst + C::kTensorBytes;
@@ -236,25 +238,74 @@ __device__ __forceinline__ bool produce_split_tiles(uint8_t* smem, uint64_t* ful
       }
     }
   }
-  return true;
 }
 
-// One thread: the tiles of a share [x, x1) of the line, segment after segment.  `skip`
-// tells which KV heads the CTA leaves out (the consumers leave out the same ones).
-template <class C, bool PAGED, class Skip>
+// One warp: the tiles of a share [x, x1) of the line, segment after segment.  Lane j holds
+// the first cache row of the segment's block 32 k + j, read while the 32 blocks before are
+// being copied: with one thread reading a tile's table entries and then issuing its copies,
+// each FP8 tile cost the producer a memory round trip, and the three CTAs of an SM drew
+// 4.8 TB/s.  Lanes 0-3 issue the copies of a tile's four blocks.
+template <class C, bool PAGED>
 __device__ __forceinline__ void produce_stream(uint8_t* smem, uint64_t* full, uint64_t* empty, const CUtensorMap* tmK,
                                                const CUtensorMap* tmV, const SplitParams& p, const StreamPlan* plan,
-                                               int x, int x1, Skip skip, int* abort_flag) {
-  int at = 0;
-  while (x < x1) {
-    const Segment s = stream_segment<PAGED>(p, plan, x, x1);
-    if (!skip(s.g)) {
-      if (!produce_split_tiles<C, PAGED, true>(smem, full, empty, tmK, tmV, p, s.b, s.g, s.tok_begin, s.tok_end,
-                                               s.n_tiles, s.sk, abort_flag, at))
-        return;
-      at += s.n_tiles;
-    }
+                                               int x, int x1, int* abort_flag) {
+  constexpr int kBlocks = kDecodeTile / kPageTokens;
+  const int lane = threadIdx.x & 31;
+  const uint64_t pol = policy_evict_first();
+  // first row, in the [rows, Hkv, d] view of the cache, of this lane's block of batch k
+  auto read_rows = [&](const Segment& s, int k) -> int {
+    const int vt = s.tok_begin + (32 * k + lane) * kPageTokens;
+    if (vt >= s.tok_end) return 0;
+    const int pos = vt + (vt >= s.sk.s16 ? s.sk.gap : 0);
+    return PAGED ? __ldg(p.page_table + (size_t)s.b * p.max_blocks + pos / kPageTokens) : s.b * p.capacity + pos;
+  };
+  Segment s = stream_segment<PAGED>(p, plan, x, x1);
+  int next_rows = read_rows(s, 0);
+  for (int at = 0;;) {
     x += s.n_tiles;
+    const Segment after = x < x1 ? stream_segment<PAGED>(p, plan, x, x1) : s;
+    int rows = 0;
+    for (int i = 0; i < s.n_tiles; ++i, ++at) {
+      const int j = i * kBlocks & 31;   // the tile's first block in its batch of 32
+      if (j == 0) {
+        rows = next_rows;
+        const int k = i * kBlocks / 32 + 1;
+        const bool same = k * (32 / kBlocks) < s.n_tiles;
+        if (same || x < x1) next_rows = read_rows(same ? s : after, same ? k : 0);
+        if constexpr (PAGED) {
+          const bool used = s.tok_begin + (i * kBlocks + lane) * kPageTokens < s.tok_end;
+          if (used && (rows < 0 || rows >= p.num_blocks)) {
+            atomicOr(p.status, DEV_PAGE_ID);
+            rows = 0;   // keep the byte count; the result is flagged invalid
+          }
+          rows *= kPageTokens;
+        }
+      }
+      const int row = __shfl_sync(0xffffffffu, rows, j + (lane & (kBlocks - 1)));
+      const int nb = min(kBlocks, (s.tok_end - (s.tok_begin + i * kDecodeTile) + kPageTokens - 1) / kPageTokens);
+      const int st = at % C::kStages;
+      bool ok = true;
+      if (lane == 0) {
+        ok = at < C::kStages || mbar_wait(&empty[st], ((at / C::kStages) - 1) & 1);
+        if (ok) {
+          mbar_arrive_expect_tx(&full[st], nb * 2 * C::kHalves * kPageTokens * 128);
+        } else {
+          atomicOr(p.status, DEV_TIMEOUT);
+          *reinterpret_cast<volatile int*>(abort_flag) = 1;
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, (int)ok, 0)) return;
+      if (lane < nb) {
+        uint8_t* kst = smem + st * C::kStageBytes + lane * kPageTokens * 128;
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h) {
+          tma_load_3d(kst + h * C::kHalfBytes, tmK, &full[st], h * 64, s.g, row, pol);
+          tma_load_3d(kst + C::kTensorBytes + h * C::kHalfBytes, tmV, &full[st], h * 64, s.g, row, pol);
+        }
+      }
+    }
+    if (x >= x1) return;
+    s = after;
   }
 }
 
@@ -294,16 +345,19 @@ inline cudaError_t launch_beside(Kernel kern, dim3 grid, int threads, int smem, 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Launch a SEL instance of a warp-level kernel: p.stream CTAs or one per chunk, one more with p.fence.
+// Launch a SEL instance of a warp-level kernel, with one CTA more if p.fence.
 template <class Kernel>
 inline cudaError_t launch_sel(Kernel kern, int threads, int smem, const CUtensorMap& tk, const CUtensorMap& tv,
                               const SplitParams& sp, int B, cudaStream_t stream) {
-  const dim3 grid = sp.stream ? dim3(sp.stream + sp.fence) : dim3(sp.max_chunks + sp.fence, sp.Hkv, B);
+  const dim3 grid = sp.stream ? dim3(sp.stream * sp.Hkv + sp.fence) : dim3(sp.max_chunks + sp.fence, sp.Hkv, B);
   return launch_beside(kern, grid, threads, smem, stream, sp.fence != 0, tk, tv, sp);
 }
 
 // FP8 caches, at most 8 query rows per KV head: the transposed-product split kernel (decode_fp8.cu)
 cudaError_t launch_decode_fp8_rows8(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int B,
-                                    bool paged, bool sel, cudaStream_t stream);
+                                    bool paged, cudaStream_t stream);
+// windowed and shared-prefix decode, at most 8 query rows per KV head (decode_rows8.cu)
+cudaError_t launch_decode_rows8(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int B, int d,
+                                bool fp8, bool paged, cudaStream_t stream);
 
 }  // namespace kvattn
