@@ -428,7 +428,7 @@ int shared_impl(const void* q, const void* k_cache, const void* v_cache, const f
   pre.sel.select = 1;
   pre.sel.fixed_len = prefix_blocks * kPageTokens;
   pre.stream = s.pre_stream;
-  pre.fence = 1;
+  pre.early = 1;
   // each sequence's own keys, and the merge of both parts
   DecodeLaunch own = pre;
   own.seqlens = seqlens_k;
@@ -449,8 +449,8 @@ int shared_impl(const void* q, const void* k_cache, const void* v_cache, const f
   own.n_chunks = s.own.n_chunks;
   own.plan = s.own.balanced ? reinterpret_cast<int*>(ws + s.own_offset + s.own.plan_offset) : nullptr;
   own.stream = s.own.stream;
-  own.fence = 0;
-  own.early = 1;
+  own.early = 0;
+  own.fence = 1;
   own.sel.fixed_len = 0;
   own.sel.skip = prefix_blocks * kPageTokens;
   own.pre_o = pre.part_o;
@@ -462,8 +462,8 @@ int shared_impl(const void* q, const void* k_cache, const void* v_cache, const f
   // side: the own part's CTAs, at most one per SM, start first and let the prefix's in at
   // once; the prefix's launch ends after the own part's, so the combine waits for both.
   cudaStream_t st_ = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_decode_split(own, st_);
-  if (e == cudaSuccess) e = launch_decode_split(pre, st_);
+  cudaError_t e = launch_decode_split(pre, st_);
+  if (e == cudaSuccess) e = launch_decode_split(own, st_);
   if (e == cudaSuccess) e = launch_decode_combine(own, st_);
   return cuda_status(e, name);
 }

@@ -107,8 +107,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
       return;
     }
   }
-  auto init_ring = [&] {
-    if (threadIdx.x == 0) {
+  auto init_ring = [&](int thread) {
+    if (threadIdx.x == thread) {
       for (int s = 0; s < C::kStages; ++s) {
         mbar_init(&full[s], 1);
         mbar_init(&empty[s], C::kConsumerWarps);
@@ -119,12 +119,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
   };
   if (SEL && p.stream) {
     __shared__ StreamPlan plan_smem;
-    if (threadIdx.x == C::kConsumerWarps * 32) {
-      prefetch_tmap(&tmK);
-      prefetch_tmap(&tmV);
-    }
-    init_ring();
-    stream_plan<PAGED>(p, &plan_smem);
+    init_ring(C::kConsumerWarps * 32);
+    if (warp == C::kConsumerWarps) stream_plan<PAGED, C::kThreads>(p, &plan_smem);
+    else stream_plan_wait<C::kThreads>();
     plan = &plan_smem;
     const int total = plan->first[p.B], n = min(p.stream, total), i = c / p.Hkv;
     if (i >= n) return;
@@ -156,15 +153,16 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
     }
   }
 
-  if (!(SEL && p.stream)) {   // else done before the plan, whose barriers cover it
-    init_ring();
+  if (!(SEL && p.stream)) {   // else the producer has done it, before the plan's barrier
+    init_ring(0);
     __syncthreads();
   }
 
   if (warp == C::kConsumerWarps) {
     // ------------------------------------------------------------ producer
     if (SEL && p.stream) {
-      produce_stream<C, PAGED>(smem, full, empty, &tmK, &tmV, p, plan, x, x1, abort_flag);
+      produce_stream<C, PAGED>(smem, full, empty, &tmK, &tmV, p, plan, stream_segment<PAGED>(p, plan, x, x1), x, x1,
+                               abort_flag);
     } else if (lane == 0) {
       produce_split_tiles<C, PAGED, SEL>(smem, full, empty, &tmK, &tmV, p, b, g, tok_begin, tok_end, n_tiles, sk,
                                          abort_flag);
@@ -270,7 +268,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
       break;
     }
     if (*reinterpret_cast<volatile int*>(abort_flag)) break;
-    const uint32_t kbase = smem_u32(smem + s * C::kStageBytes);
+    // SEL: a stage holds block after block of 16 rows, each span of them together
+    constexpr int kSpan = SEL ? kPageTokens * 128 : C::kHalfBytes;
+    const int block0 = SEL ? wsub * (C::kHalves - 1) * kSpan : 0;
+    const uint32_t kbase = smem_u32(smem + s * C::kStageBytes) + block0;
     const uint32_t vbase = kbase + C::kTensorBytes;
     const int tok_base = tok_begin + i * kDecodeTile + wsub * 16;
 
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
       for (int kk = 0; kk < D / 16; ++kk) {
         const int chunk16 = kk * 2 + (lm & 1);             // 16-byte chunk along d
         const int h = chunk16 >> 3, cw = chunk16 & 7;
-        const uint32_t addr = kbase + h * C::kHalfBytes + trow * 128 + ((cw ^ (trow & 7)) << 4);
+        const uint32_t addr = kbase + h * kSpan + trow * 128 + ((cw ^ (trow & 7)) << 4);
         uint32_t b0, b1, b2, b3;
         ldsm_x4(addr, b0, b1, b2, b3);
         mma_bf16_16816(sacc[0], qa[kk], b0, b1);
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
       for (int nn = 0; nn < D / 16; ++nn) {
         const int chunk16 = nn * 2 + (lm >> 1);
         const int h = chunk16 >> 3, cw = chunk16 & 7;
-        const uint32_t addr = vbase + h * C::kHalfBytes + vrow * 128 + ((cw ^ (vrow & 7)) << 4);
+        const uint32_t addr = vbase + h * kSpan + vrow * 128 + ((cw ^ (vrow & 7)) << 4);
         ldsm_x4_t(addr, vb[nn][0], vb[nn][1], vb[nn][2], vb[nn][3]);
         if (tail) {
           vb[nn][0] &= keep_a;
@@ -912,6 +913,18 @@ SplitParams split_params(const DecodeLaunch& a) {
 
 }  // namespace
 
+namespace {
+int device_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
+    cudaGetLastError();   // no device here (workspace sizing on a host without one): a B200's 148 SMs
+    sms = 148;
+  }
+  return sms;
+}
+}  // namespace
+
 int decode_chunk_tokens(int B, int T, int G, int Hkv, int max_seqlen, int num_splits, bool fp8) {
   int chunk;
   if (num_splits > 0) {
@@ -939,23 +952,11 @@ int decode_chunk_tokens(int B, int T, int G, int Hkv, int max_seqlen, int num_sp
   return chunk < kDecodeTcTile ? kDecodeTcTile : chunk;
 }
 
-namespace {
-int device_sms() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
-    cudaGetLastError();   // no device here (workspace sizing on a host without one): a B200's 148 SMs
-    sms = 148;
-  }
-  return sms;
-}
-}  // namespace
-
 int prefix_chunk_tokens(int tokens, int G, int Hkv, int prefix, int num_splits, bool fp8) {
   if (num_splits > 0 || !decode_uses_tc(G * tokens, fp8))
     return decode_chunk_tokens(1, tokens, G, Hkv, prefix, num_splits, fp8);
   const long long units = (long long)Hkv * decode_row_tiles(tokens, G);
-  const long long items = 3LL * device_sms();
+  const long long items = device_sms();
   const long long chunk = std::max((prefix * units + items - 1) / items, 128LL);
   return (int)((chunk + kDecodeTcTile - 1) / kDecodeTcTile * kDecodeTcTile);
 }
@@ -985,7 +986,14 @@ cudaError_t launch_decode_split(const DecodeLaunch& a, cudaStream_t stream) {
   const int eb = a.fp8 ? 1 : 2;   // bytes per cached element
   const uint64_t s1 = (uint64_t)a.d * eb, s2 = (uint64_t)a.Hkv * a.d * eb;
   const uint32_t box0 = 128 / eb;  // one 128-byte swizzle span
-  if (encode_tmap_3d(&tk, a.k, a.d, a.Hkv, rows, s1, s2, box0, 1, box_rows, eb) ||
+  if (a.sel.select && !tc) {
+    // {span, head, row, spans of a row}: one copy takes a block's rows span by span
+    const cuuint64_t dims[4] = {box0, (cuuint64_t)a.Hkv, rows, (cuuint64_t)(s1 / 128)};
+    const cuuint64_t strides[3] = {s1, s2, 128};
+    const cuuint32_t box[4] = {box0, 1, (cuuint32_t)kPageTokens, (cuuint32_t)(s1 / 128)};
+    if (encode_tmap_nd(&tk, a.k, 4, dims, strides, box, eb) || encode_tmap_nd(&tv, a.v, 4, dims, strides, box, eb))
+      return cudaErrorInvalidValue;
+  } else if (encode_tmap_3d(&tk, a.k, a.d, a.Hkv, rows, s1, s2, box0, 1, box_rows, eb) ||
       encode_tmap_3d(&tv, a.v, a.d, a.Hkv, rows, s1, s2, box0, 1, box_rows, eb))
     return cudaErrorInvalidValue;
 
@@ -1028,8 +1036,11 @@ cudaError_t launch_decode_combine(const DecodeLaunch& a, cudaStream_t stream) {
     row_chunks = sp.stream ? share(sp.stream, a.B) : (a.balanced ? share(a.n_chunks, a.B) : sp.max_chunks);
     if (a.pre_o) row_chunks += a.pre_stream ? std::min(a.pre_stream, a.pre_tiles) : a.pre_chunks;
   }
-  while (wpr < 8 && wpr * 4 < row_chunks) wpr *= 2;
   const long long rows_out = (long long)a.B * a.T * a.Hq;
+  // SEL, many rows: as few waves of CTAs (2 x 8 warps per SM) as possible.  2048 rows of 23
+  // chunks took 29 us with 8 warps a row, seven waves that each wait for their loads
+  const long long warps = a.sel.select ? 16LL * device_sms() : INT64_MAX;
+  while (wpr < 8 && wpr * 4 < row_chunks && rows_out * wpr * 2 <= warps) wpr *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((rows_out * wpr + 7) / 8));
   cfg.blockDim = dim3(256);

@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
                         const SplitParams p) {
   using C = Rows8Cfg<D, FP8>;
   constexpr int kC = C::kConsumerWarps * 32;
+  constexpr int kSpan = kPageTokens * 128;   // a 128-byte span of a block's 16 rows
   extern __shared__ uint8_t smem_raw[];
   __shared__ StreamPlan plan;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -104,7 +105,8 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
   int x = 0, x1 = 0;   // p.stream: this CTA's share of the tiles
   Segment sg;
   if (p.stream) {
-    stream_plan<PAGED>(p, &plan);
+    if (warp == C::kConsumerWarps) stream_plan<PAGED, C::kThreads>(p, &plan);
+    else stream_plan_wait<C::kThreads>();
     const int total = plan.first[p.B], n = min(p.stream, total), i = c / p.Hkv;
     if (i >= n) return;
     x = stream_begin(i, n, total);
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
 
   if (warp == C::kConsumerWarps) {
     if (p.stream) {
-      produce_stream<C, PAGED>(smem, full, empty, &tmK, &tmV, p, &plan, x, x1, abort_flag);
+      produce_stream<C, PAGED>(smem, full, empty, &tmK, &tmV, p, &plan, sg, x, x1, abort_flag);
     } else if (lane == 0) {
       produce_split_tiles<C, PAGED, true>(smem, full, empty, &tmK, &tmV, p, sg.b, sg.g, sg.tok_begin, sg.tok_end,
                                           sg.n_tiles, sg.sk, abort_flag);
@@ -201,7 +203,8 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
         break;
       }
       if (*reinterpret_cast<volatile int*>(abort_flag)) break;
-      const uint32_t kbase = smem_u32(smem + s * C::kStageBytes);
+      // this warp's 16 tokens: C::kHalves spans of 16 rows
+      const uint32_t kbase = smem_u32(smem + s * C::kStageBytes) + wsub * (C::kHalves * kSpan);
       const uint32_t vbase = kbase + C::kTensorBytes;
       const int tok_base = sg.tok_begin + i * kDecodeTile + wsub * 16;
       const bool inside = tok_base + 16 <= first_end && (tok_base >= last_lo || tok_base + 16 <= p.sel.sinks);
@@ -213,7 +216,7 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
         uint32_t kw[2][8];
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
-          const uint32_t ra = kbase + (wsub * 16 + rr * 8 + gid) * 128;
+          const uint32_t ra = kbase + (rr * 8 + gid) * 128;
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             const uint4 w = lds128(ra + (((tig + 4 * hh) ^ gid) << 4));
@@ -231,13 +234,13 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
           mma_f16_16816((kk & 1) ? sb : sa, a, qb[kk][0], qb[kk][1]);
         }
       } else {
-        const int trow = wsub * 16 + (lm & 1) * 8 + lr;   // key; matrices 2 and 3 are the next 16 bytes of d
+        const int trow = (lm & 1) * 8 + lr;   // key; matrices 2 and 3 are the next 16 bytes of d
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const int chunk16 = kk * 2 + (lm >> 1);
           const int h = chunk16 >> 3, cw = chunk16 & 7;
           uint32_t a[4];
-          ldsm_x4(kbase + h * C::kHalfBytes + trow * 128 + ((cw ^ (trow & 7)) << 4), a[0], a[1], a[2], a[3]);
+          ldsm_x4(kbase + h * kSpan + trow * 128 + ((cw ^ (trow & 7)) << 4), a[0], a[1], a[2], a[3]);
           mma_bf16_16816((kk & 1) ? sb : sa, a, qb[kk][0], qb[kk][1]);
         }
       }
@@ -249,8 +252,7 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int key = 2 * tig + (q & 1) + 8 * (q >> 1);
-          const int vrow = wsub * 16 + key;
-          uint4 w = lds128(vbase + vrow * 128 + ((gid ^ (vrow & 7)) << 4));
+          uint4 w = lds128(vbase + key * 128 + ((gid ^ (key & 7)) << 4));
           if (!inside && dead(tok_base + key)) w = make_uint4(0u, 0u, 0u, 0u);
           vw[q][0] = w.x;
           vw[q][1] = w.y;
@@ -259,12 +261,12 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
         }
       } else {
         // V^T fragments: matrices (keys 0-7 | 8-15) x (d 0-7 | 8-15), transposed on the way
-        const int vrow = wsub * 16 + (lm >> 1) * 8 + lr;
+        const int vrow = (lm >> 1) * 8 + lr;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
           const int chunk16 = j * 2 + (lm & 1);
           const int h = chunk16 >> 3, cw = chunk16 & 7;
-          ldsm_x4_t(vbase + h * C::kHalfBytes + vrow * 128 + ((cw ^ (vrow & 7)) << 4), vw[j][0], vw[j][1], vw[j][2],
+          ldsm_x4_t(vbase + h * kSpan + vrow * 128 + ((cw ^ (vrow & 7)) << 4), vw[j][0], vw[j][1], vw[j][2],
                     vw[j][3]);
         }
         if (!inside) {

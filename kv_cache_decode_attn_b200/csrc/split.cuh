@@ -109,35 +109,39 @@ __device__ __forceinline__ int stream_cta(int x, int n, int total) {
   return x < wide ? x / (share + 1) : (x - total % n) / share;
 }
 
-// All threads of the CTA: tile counts of the sequences, summed (0 for an invalid length,
-// which CTA 0 reports).
-template <bool PAGED>
+// One warp (the producer): tile counts of the sequences, summed (0 for an invalid length,
+// which block 0 reports).  The CTA's other warps wait for it in stream_plan_wait, while
+// this one goes on to its first copies.
+template <bool PAGED, int kThreads>
 __device__ __forceinline__ void stream_plan(const SplitParams& p, StreamPlan* plan) {
-  for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
-    const SeqKeys k = seq_keys<true>(p.sel, p.seqlens, i, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
-    if (k.bad && blockIdx.x == 0) atomicOr(p.status, DEV_SEQLEN);
-    plan->first[i + 1] = k.bad ? 0 : (k.L + kDecodeTile - 1) / kDecodeTile;
-    plan->len[i] = p.sel.fixed_len ? 0 : p.seqlens[i];
-  }
-  if (threadIdx.x == 0) plan->first[0] = 0;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int carry = 0;
-    for (int base = 0; base < p.B; base += 32) {
-      const int i = base + lane;
-      int v = i < p.B ? plan->first[i + 1] : 0;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v += u;
-      }
-      v += carry;
-      if (i < p.B) plan->first[i + 1] = v;
-      carry = __shfl_sync(0xffffffffu, v, 31);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) plan->first[0] = 0;
+  int carry = 0;
+  for (int base = 0; base < p.B; base += 32) {
+    const int i = base + lane;
+    int v = 0;
+    if (i < p.B) {
+      if (!p.sel.fixed_len) plan->len[i] = p.seqlens[i];
+      const SeqKeys k = seq_keys<true>(p.sel, plan->len, i, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
+      if (k.bad && blockIdx.x == 0) atomicOr(p.status, DEV_SEQLEN);
+      v = k.bad ? 0 : (k.L + kDecodeTile - 1) / kDecodeTile;
     }
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, off);
+      if (lane >= off) v += u;
+    }
+    v += carry;
+    if (i < p.B) plan->first[i + 1] = v;
+    carry = __shfl_sync(0xffffffffu, v, 31);
   }
-  __syncthreads();
+  __syncwarp();
+  asm volatile("barrier.cta.arrive 2, %0;" ::"n"(kThreads) : "memory");
+}
+
+template <int kThreads>
+__device__ __forceinline__ void stream_plan_wait() {
+  asm volatile("barrier.cta.sync 2, %0;" ::"n"(kThreads) : "memory");
 }
 
 // A run of consecutive tiles of one (sequence, KV head): keys [tok_begin, tok_end), whose
@@ -173,7 +177,8 @@ __device__ __forceinline__ Segment stream_segment(const SplitParams& p, const St
 // C::kStages stages (K then V, C::kHalves 128-byte swizzle spans per token row;
 // contiguous: one 64-row box per span; paged: one 16-row box per physical
 // block, its page-table entry bounds-checked first; SEL instances: one 16-row box per
-// selected block in either layout), evict-first L2 policy.  A
+// selected block in either layout, both spans of a row in one copy: the stage then holds
+// block after block, and each span's 16 rows together), evict-first L2 policy.  A
 // stage is refilled once the consumers released it (empty barrier); a wait that
 // gives up sets DEV_TIMEOUT and the abort flag.
 template <class C, bool PAGED, bool SEL>
@@ -230,6 +235,11 @@ __device__ __forceinline__ void produce_split_tiles(uint8_t* smem, uint64_t* ful
           blk = 0;   // keep the byte count; the result is flagged invalid
         }
         const int row = PAGED ? blk * kPageTokens : blk;
+        if constexpr (SEL) {
+          tma_load_4d(kst + j * C::kHalves * kPageTokens * 128, tmK, &full[s], 0, g, row, 0, pol);
+          tma_load_4d(vst + j * C::kHalves * kPageTokens * 128, tmV, &full[s], 0, g, row, 0, pol);
+          continue;
+        }
 #pragma unroll
         for (int h = 0; h < C::kHalves; ++h) {
           tma_load_3d(kst + h * C::kHalfBytes + j * kPageTokens * 128, tmK, &full[s], h * 64, g, row, pol);
@@ -240,15 +250,16 @@ __device__ __forceinline__ void produce_split_tiles(uint8_t* smem, uint64_t* ful
   }
 }
 
-// One warp: the tiles of a share [x, x1) of the line, segment after segment.  Lane j holds
+// One warp: the tiles of a share [x, x1) of the line, segment after segment, s the first.  Lane j holds
 // the first cache row of the segment's block 32 k + j, read while the 32 blocks before are
 // being copied: with one thread reading a tile's table entries and then issuing its copies,
 // each FP8 tile cost the producer a memory round trip, and the three CTAs of an SM drew
-// 4.8 TB/s.  Lanes 0-3 issue the copies of a tile's four blocks.
+// 4.8 TB/s.  Lane 0 issues the copies (from lanes of their own
+// they took 95 cycles each: their operands are warp-uniform, so lanes take turns).
 template <class C, bool PAGED>
 __device__ __forceinline__ void produce_stream(uint8_t* smem, uint64_t* full, uint64_t* empty, const CUtensorMap* tmK,
                                                const CUtensorMap* tmV, const SplitParams& p, const StreamPlan* plan,
-                                               int x, int x1, int* abort_flag) {
+                                               Segment s, int x, int x1, int* abort_flag) {
   constexpr int kBlocks = kDecodeTile / kPageTokens;
   const int lane = threadIdx.x & 31;
   const uint64_t pol = policy_evict_first();
@@ -259,19 +270,15 @@ __device__ __forceinline__ void produce_stream(uint8_t* smem, uint64_t* full, ui
     const int pos = vt + (vt >= s.sk.s16 ? s.sk.gap : 0);
     return PAGED ? __ldg(p.page_table + (size_t)s.b * p.max_blocks + pos / kPageTokens) : s.b * p.capacity + pos;
   };
-  Segment s = stream_segment<PAGED>(p, plan, x, x1);
+  Segment after = s;
   int next_rows = read_rows(s, 0);
   for (int at = 0;;) {
     x += s.n_tiles;
-    const Segment after = x < x1 ? stream_segment<PAGED>(p, plan, x, x1) : s;
     int rows = 0;
     for (int i = 0; i < s.n_tiles; ++i, ++at) {
       const int j = i * kBlocks & 31;   // the tile's first block in its batch of 32
       if (j == 0) {
         rows = next_rows;
-        const int k = i * kBlocks / 32 + 1;
-        const bool same = k * (32 / kBlocks) < s.n_tiles;
-        if (same || x < x1) next_rows = read_rows(same ? s : after, same ? k : 0);
         if constexpr (PAGED) {
           const bool used = s.tok_begin + (i * kBlocks + lane) * kPageTokens < s.tok_end;
           if (used && (rows < 0 || rows >= p.num_blocks)) {
@@ -281,7 +288,9 @@ __device__ __forceinline__ void produce_stream(uint8_t* smem, uint64_t* full, ui
           rows *= kPageTokens;
         }
       }
-      const int row = __shfl_sync(0xffffffffu, rows, j + (lane & (kBlocks - 1)));
+      int row[kBlocks];
+#pragma unroll
+      for (int e = 0; e < kBlocks; ++e) row[e] = __shfl_sync(0xffffffffu, rows, j + e);
       const int nb = min(kBlocks, (s.tok_end - (s.tok_begin + i * kDecodeTile) + kPageTokens - 1) / kPageTokens);
       const int st = at % C::kStages;
       bool ok = true;
@@ -295,12 +304,22 @@ __device__ __forceinline__ void produce_stream(uint8_t* smem, uint64_t* full, ui
         }
       }
       if (!__shfl_sync(0xffffffffu, (int)ok, 0)) return;
-      if (lane < nb) {
-        uint8_t* kst = smem + st * C::kStageBytes + lane * kPageTokens * 128;
+      if (lane == 0) {
 #pragma unroll
-        for (int h = 0; h < C::kHalves; ++h) {
-          tma_load_3d(kst + h * C::kHalfBytes, tmK, &full[st], h * 64, s.g, row, pol);
-          tma_load_3d(kst + C::kTensorBytes + h * C::kHalfBytes, tmV, &full[st], h * 64, s.g, row, pol);
+        for (int e = 0; e < kBlocks; ++e) {
+          if (e >= nb) break;
+          uint8_t* kst = smem + st * C::kStageBytes + e * C::kHalves * kPageTokens * 128;
+          tma_load_4d(kst, tmK, &full[st], 0, s.g, row[e], 0, pol);
+          tma_load_4d(kst + C::kTensorBytes, tmV, &full[st], 0, s.g, row[e], 0, pol);
+        }
+      }
+      if (j == 0) {   // the batch after this one
+        const int k = i * kBlocks / 32 + 1;
+        if (k * (32 / kBlocks) < s.n_tiles) {
+          next_rows = read_rows(s, k);
+        } else if (x < x1) {
+          after = stream_segment<PAGED>(p, plan, x, x1);
+          next_rows = read_rows(after, 0);
         }
       }
     }
