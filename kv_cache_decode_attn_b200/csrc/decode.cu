@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
   const StreamPlan* plan = nullptr;
   int x = 0, x1 = 0;   // p.stream: this CTA's share of the tiles
   if constexpr (SEL) {
+    if (!p.fence) grid_dependency_wait();   // launched early too; with p.fence the kernel before has waited
     if (p.early) launch_dependents();
     if (p.fence && c == (p.stream ? p.stream * p.Hkv : p.max_chunks)) {
       if (g == 0 && b == 0) grid_dependency_wait();

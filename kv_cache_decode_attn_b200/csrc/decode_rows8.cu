@@ -87,11 +87,6 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
   const int lane = threadIdx.x & 31;
   const int c = blockIdx.x;
 
-  if (p.early) launch_dependents();
-  if (p.fence && c == (p.stream ? p.stream * p.Hkv : p.max_chunks)) {
-    if (blockIdx.y == 0 && blockIdx.z == 0) grid_dependency_wait();
-    return;
-  }
   if (threadIdx.x == kC) {
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
@@ -101,6 +96,12 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
     }
     *abort_flag = 0;
     fence_mbar_init();
+  }
+  if (!p.fence) grid_dependency_wait();   // launched early too; with p.fence the kernel before has waited
+  if (p.early) launch_dependents();
+  if (p.fence && c == (p.stream ? p.stream * p.Hkv : p.max_chunks)) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) grid_dependency_wait();
+    return;
   }
   int x = 0, x1 = 0;   // p.stream: this CTA's share of the tiles
   Segment sg;

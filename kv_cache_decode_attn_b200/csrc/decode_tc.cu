@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
   int c, rt, g, b, chunk;
   size_t item;
   if constexpr (SEL) {
+    if (!p.fence) grid_dependency_wait();   // launched early too; with p.fence the kernel before has waited
     if (p.early) launch_dependents();
     if (p.fence && blockIdx.x == gridDim.x - 1) {
       if (blockIdx.y == 0 && blockIdx.z == 0) grid_dependency_wait();
@@ -830,7 +831,7 @@ cudaError_t run_tc_as(const DecodeLaunch& a, const CUtensorMap& tk, const CUtens
   if (a.balanced) grid = dim3((unsigned)a.n_chunks * a.Hkv);
   if constexpr (SEL) {
     grid.x += a.fence;
-    return launch_beside(kern, grid, tc_threads<FP8>(), C::kSmemBytes, stream, a.fence != 0, tq, tk, tv, p);
+    return launch_beside(kern, grid, tc_threads<FP8>(), C::kSmemBytes, stream, true, tq, tk, tv, p);
   }
   kern<<<grid, tc_threads<FP8>(), C::kSmemBytes, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();

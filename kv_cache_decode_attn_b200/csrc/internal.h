@@ -67,6 +67,25 @@ struct KeySelect {
   int fixed_len = 0;   // > 0: every sequence has exactly this many keys (seqlens is not read)
 };
 
+// Launch a kernel.  `beside`: its CTAs may start before the kernel in front of it in the
+// stream has ended (programmatic dependent launch); it waits itself, where it has to.
+template <class Kernel, class... Args>
+inline cudaError_t launch_beside(Kernel kern, dim3 grid, int threads, int smem, cudaStream_t stream, bool beside,
+                                 const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 struct DecodeLaunch {
   const void* q;
   const void* k;          // contiguous cache or paged pool

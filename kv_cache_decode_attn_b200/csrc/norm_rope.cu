@@ -11,7 +11,12 @@
 //
 // d / 16 threads share a row, 16 values each, chosen so that a thread holds both
 // members of each of its pairs: only the sum of squares crosses threads (2 or 3
-// shuffles).
+// shuffles).  A warp takes the same 4 (d = 128) or 8 heads of kTokens consecutive tokens,
+// the next token's values on their way while one is computed; the weights are unpacked
+// once, positions and addresses step from token to token, and values are computed in
+// pairs (f32x2).  Bound by HBM once that is so: with indexes divided out per row and single
+// fp32 operations the issue slots were 72 % busy and 4 x 4096 tokens of 32 + 8 + 8 heads
+// (405 MB) took 93 to 130 us.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -21,149 +26,233 @@
 namespace kvattn {
 namespace {
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* src, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(src);
+// Two fp32 values in one register pair.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 parts(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 neg2(F2 a) { return a ^ 0x8000000080000000ull; }
+
+// 8 values, as 4 pairs of neighbours
+__device__ __forceinline__ void unpack8(uint4 u, F2 (&x)[4]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ void load8f(const float* src, F2 (&x)[4]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(src)), b = __ldg(reinterpret_cast<const float4*>(src) + 1);
+  x[0] = f2(a.x, a.y);
+  x[1] = f2(a.z, a.w);
+  x[2] = f2(b.x, b.y);
+  x[3] = f2(b.z, b.w);
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* dst, const F2 (&x)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = parts(x[i]);
+    w[i] = pack_bf16x2(v.x, v.y);
+  }
+  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // codes of x / s, each quotient one IEEE division
-__device__ __forceinline__ void store8_e4m3(uint8_t* dst, const float (&x)[8], float s) {
+__device__ __forceinline__ void store8_e4m3(uint8_t* dst, const F2 (&x)[4], float s) {
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = f32x2_to_e4m3x2(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s));
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = parts(x[i]);
+    c[i] = f32x2_to_e4m3x2(__fdiv_rn(v.x, s), __fdiv_rn(v.y, s));
+  }
   *reinterpret_cast<uint2*>(dst) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-template <int D>
-__global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeLaunch a) {
-  constexpr int kLanes = D / 16;   // threads per row
-  const int rows_per_token = a.Hq + a.Hkv * (a.cached ? 2 : 1);   // q heads, K heads, V heads
-  const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / kLanes;
-  const int j = threadIdx.x % kLanes;
-  const long long n_rows = (long long)a.B * a.T * rows_per_token;
-  const bool live = row < n_rows;
-  const long long tok = live ? row / rows_per_token : 0;
-  const int h = live ? (int)(row - tok * rows_per_token) : 0;
-  const int b = (int)(tok / a.T), t = (int)(tok - (long long)b * a.T);
-  const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
-  const int g = is_q ? 0 : (is_v ? h - a.Hq - a.Hkv : h - a.Hq);   // KV head
+// head_blocks: CTAs per token group, each with blockDim / 32 groups of heads
+template <int D, int kTokens, bool CACHED, bool FP8>
+__global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeLaunch a, int head_blocks) {
+  constexpr int kLanes = D / 16;       // threads per row
+  constexpr int kHeads = 32 / kLanes;  // rows (heads of one token) per warp
+  const int tg = blockIdx.x / head_blocks;
+  const int lane = threadIdx.x & 31, j = lane & (kLanes - 1);
+  const int row = ((blockIdx.x - tg * head_blocks) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kHeads + lane / kLanes;
+  const bool live = row < a.Hq + a.Hkv * (CACHED ? 2 : 1);        // q heads, K heads, V heads
+  const int h = live ? row : 0;
+  const bool is_q = h < a.Hq, is_v = CACHED && h >= a.Hq + a.Hkv;
+  const int g = is_q ? h : (is_v ? h - a.Hq - a.Hkv : h - a.Hq);   // head among its kind
+  int tok = tg * kTokens;
+  const int n_tok = min(kTokens, a.B * a.T - tok);
+  int b = tok / a.T, t = tok - b * a.T;
 
   // this thread's two vectors of 8 values: both halves of its rotated pairs, or (past the
   // rotated part, or with adjacent pairs) two neighbouring vectors
   const int n_rot = a.interleaved ? 0 : a.rot / 16;   // vector pairs (v, v + n_rot)
   const int v0 = j < n_rot ? j : 2 * j, v1 = j < n_rot ? j + n_rot : 2 * j + 1;
+  const bool turns = !is_v && (a.interleaved ? 16 * j < a.rot : j < n_rot);   // rot is a multiple of 16
 
-  const __nv_bfloat16* src = is_q   ? a.q + tok * a.q_stride + (long long)h * D
-                             : is_v ? a.v + tok * a.v_stride + (long long)g * D
-                                    : a.k + tok * a.k_stride + (long long)g * D;
-  float x0[8], x1[8];
-  load8(src + 8 * v0, x0);
-  load8(src + 8 * v1, x1);
-  const long long pos = (a.pos0 ? (long long)__ldg(a.pos0 + b) : 0) + t;
-  const bool pos_ok = a.rot == 0 || (pos >= 0 && pos < a.rope_rows);
-
-  const __nv_bfloat16* w = is_q ? a.q_weight : (is_v ? nullptr : a.k_weight);
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss += x0[i] * x0[i] + x1[i] * x1[i];
-#pragma unroll
-  for (int off = 1; off < kLanes; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-  if (!live) return;
-  if (w) {
-    const float r = rsqrtf(ss * (1.f / D) + a.eps);
-    float w0[8], w1[8];
-    load8(w + 8 * v0, w0);
-    load8(w + 8 * v1, w1);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x0[i] *= r * w0[i];
-      x1[i] *= r * w1[i];
-    }
+  const long long stride = is_q ? a.q_stride : (is_v ? a.v_stride : a.k_stride);
+  const __nv_bfloat16* src = (is_q ? a.q : (is_v ? a.v : a.k)) + tok * stride + g * D;
+  grid_dependency_wait();              // launched while the kernel before ends
+  uint4 n0 = *reinterpret_cast<const uint4*>(src + 8 * v0), n1 = *reinterpret_cast<const uint4*>(src + 8 * v1);
+  int first = a.pos0 ? __ldg(a.pos0 + b) : 0;
+  const __nv_bfloat16* weight = is_q ? a.q_weight : (is_v ? nullptr : a.k_weight);
+  F2 w0[4], w1[4];
+  if (weight) {
+    unpack8(*reinterpret_cast<const uint4*>(weight + 8 * v0), w0);
+    unpack8(*reinterpret_cast<const uint4*>(weight + 8 * v1), w1);
   }
-  if (!is_v && pos_ok && a.rot > 0) {
-    const float* tab = a.rope + pos * a.rot;
-    if (!a.interleaved) {
-      if (j < n_rot) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float c = __ldg(tab + 8 * j + i), s = __ldg(tab + a.rot / 2 + 8 * j + i);
-          const float p = x0[i], q = x1[i];
-          x0[i] = p * c - q * s;
-          x1[i] = q * c + p * s;
-        }
+  const bool any_weight = __any_sync(0xffffffffu, weight != nullptr);
+  float scale = 0.f;
+  bool scale_ok = true;
+  if (FP8 && !is_q) {
+    const float ks = __ldg(a.k_scale + g), vs = __ldg(a.v_scale + g);
+    scale_ok = ks > 0.f && ks <= 3.402823466e38f && vs > 0.f && vs <= 3.402823466e38f;
+    scale = is_v ? vs : ks;
+  }
+  // dense rows (q_out, k_out) step from token to token
+  const bool dense = is_q || !CACHED;
+  const int heads = is_q ? a.Hq : a.Hkv;
+  __nv_bfloat16* out = (is_q ? a.q_out : a.k_out) + ((long long)tok * heads + g) * D;
+
+#pragma unroll 1
+  for (int n = 0; n < n_tok; ++n) {
+    const uint4 u0 = n0, u1 = n1;
+    const int at = first;
+    const int bb = b, tt = t;
+    if (kTokens > 1) {                 // the next token
+      if (++t == a.T) {
+        t = 0;
+        ++b;
       }
-    } else {
-      auto turn = [&](float (&x)[8], int v) {
-        if (8 * v >= a.rot) return;
+      if (n + 1 < n_tok) {
+        src += stride;
+        n0 = *reinterpret_cast<const uint4*>(src + 8 * v0);
+        n1 = *reinterpret_cast<const uint4*>(src + 8 * v1);
+        if (t == 0 && a.pos0) first = __ldg(a.pos0 + b);
+      }
+    }
+    const long long pos = (long long)at + tt;
+    const bool pos_ok = a.rot == 0 || (pos >= 0 && pos < a.rope_rows);
+    F2 c[4], s[4];
+    if (turns && pos_ok) {
+      const float* tab = a.rope + pos * a.rot + 8 * j;
+      load8f(tab, c);
+      load8f(tab + a.rot / 2, s);
+    }
+    F2 x0[4], x1[4];
+    unpack8(u0, x0);
+    unpack8(u1, x1);
+    if (any_weight) {
+      F2 sq = mul2(x0[0], x0[0]);
+#pragma unroll
+      for (int i = 1; i < 4; ++i) sq = fma2(x0[i], x0[i], sq);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sq = fma2(x1[i], x1[i], sq);
+      float ss = parts(sq).x + parts(sq).y;
+#pragma unroll
+      for (int off = 1; off < kLanes; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+      if (weight) {
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        const F2 rr = f2(r, r);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float c = __ldg(tab + 4 * v + i), s = __ldg(tab + a.rot / 2 + 4 * v + i);
-          const float p = x[2 * i], q = x[2 * i + 1];
-          x[2 * i] = p * c - q * s;
-          x[2 * i + 1] = q * c + p * s;
+          x0[i] = mul2(x0[i], mul2(w0[i], rr));
+          x1[i] = mul2(x1[i], mul2(w1[i], rr));
         }
-      };
-      turn(x0, v0);
-      turn(x1, v1);
+      }
     }
-  }
-  if (!pos_ok) {
-    if (j == 0) atomicOr(a.status, DEV_POSITION);
-    if (!is_q && a.cached) return;   // the cache keeps what it holds
+    if (turns && pos_ok) {
+      if (!a.interleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x0[i] = x1[i] = NAN;
-  }
-  if (is_q || !a.cached) {
-    __nv_bfloat16* dst = is_q ? a.q_out + (tok * a.Hq + h) * D : a.k_out + (tok * a.Hkv + g) * D;
-    store8(dst + 8 * v0, x0);
-    store8(dst + 8 * v1, x1);
-    return;
-  }
-  // K or V: the token's row of the cache, as kv_append places it
-  long long dst_row;
-  if (!a.page_table) {
-    if (pos < 0 || pos >= a.capacity) {
-      if (j == 0) atomicOr(a.status, DEV_APPEND_RANGE);
-      return;
+        for (int i = 0; i < 4; ++i) {
+          const F2 p = x0[i], q = x1[i];
+          x0[i] = fma2(neg2(q), s[i], mul2(p, c[i]));
+          x1[i] = fma2(p, s[i], mul2(q, c[i]));
+        }
+      } else {
+        auto turn = [](F2 x, float c, float s) {
+          const float2 v = parts(x);
+          return f2(v.x * c - v.y * s, v.y * c + v.x * s);
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 ca = parts(c[i / 2]), sa = parts(s[i / 2]), cb = parts(c[2 + i / 2]), sb = parts(s[2 + i / 2]);
+          x0[i] = turn(x0[i], i & 1 ? ca.y : ca.x, i & 1 ? sa.y : sa.x);
+          x1[i] = turn(x1[i], i & 1 ? cb.y : cb.x, i & 1 ? sb.y : sb.x);
+        }
+      }
     }
-    dst_row = ((long long)b * a.capacity + pos) * a.Hkv + g;
-  } else {
-    const long long blk_idx = pos / kPageTokens;
-    if (pos < 0 || blk_idx >= a.max_blocks) {
-      if (j == 0) atomicOr(a.status, DEV_APPEND_RANGE);
-      return;
+    __nv_bfloat16* const dst_dense = out;
+    if (dense) out += heads * D;
+    if (!live) continue;
+    if (!pos_ok) {
+      if (j == 0) atomicOr(a.status, DEV_POSITION);
+      if (!dense) continue;   // the cache keeps what it holds
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x0[i] = x1[i] = f2(NAN, NAN);
     }
-    const int blk = __ldg(a.page_table + (long long)b * a.max_blocks + blk_idx);
-    if (blk < 0 || blk >= a.num_blocks) {
-      if (j == 0) atomicOr(a.status, DEV_PAGE_ID);
-      return;
+    if (dense) {
+      store8(dst_dense + 8 * v0, x0);
+      store8(dst_dense + 8 * v1, x1);
+      continue;
     }
-    dst_row = ((long long)blk * kPageTokens + pos % kPageTokens) * a.Hkv + g;
-  }
-  void* cache = is_v ? a.v_cache : a.k_cache;
-  if (a.fp8) {
-    const float sk = __ldg(a.k_scale + g), sv = __ldg(a.v_scale + g);
-    if (!(sk > 0.f && sk <= 3.402823466e38f && sv > 0.f && sv <= 3.402823466e38f)) {
-      if (j == 0) atomicOr(a.status, DEV_SCALE);
-      return;
+    // K or V: the token's row of the cache, as kv_append places it
+    long long dst_row;
+    if (!a.page_table) {
+      if (pos < 0 || pos >= a.capacity) {
+        if (j == 0) atomicOr(a.status, DEV_APPEND_RANGE);
+        continue;
+      }
+      dst_row = ((long long)bb * a.capacity + pos) * a.Hkv + g;
+    } else {
+      if (pos < 0 || pos >= (long long)a.max_blocks * kPageTokens) {
+        if (j == 0) atomicOr(a.status, DEV_APPEND_RANGE);
+        continue;
+      }
+      const int blk = __ldg(a.page_table + (long long)bb * a.max_blocks + pos / kPageTokens);
+      if (blk < 0 || blk >= a.num_blocks) {
+        if (j == 0) atomicOr(a.status, DEV_PAGE_ID);
+        continue;
+      }
+      dst_row = ((long long)blk * kPageTokens + pos % kPageTokens) * a.Hkv + g;
     }
-    uint8_t* dst = static_cast<uint8_t*>(cache) + dst_row * D;
-    store8_e4m3(dst + 8 * v0, x0, is_v ? sv : sk);
-    store8_e4m3(dst + 8 * v1, x1, is_v ? sv : sk);
-  } else {
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(cache) + dst_row * D;
-    store8(dst + 8 * v0, x0);
-    store8(dst + 8 * v1, x1);
+    void* cache = is_v ? a.v_cache : a.k_cache;
+    if constexpr (FP8) {
+      if (!scale_ok) {
+        if (j == 0) atomicOr(a.status, DEV_SCALE);
+        continue;
+      }
+      uint8_t* dst = static_cast<uint8_t*>(cache) + dst_row * D;
+      store8_e4m3(dst + 8 * v0, x0, scale);
+      store8_e4m3(dst + 8 * v1, x1, scale);
+    } else {
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(cache) + dst_row * D;
+      if (is_v) {   // as it came
+        *reinterpret_cast<uint4*>(dst + 8 * v0) = u0;
+        *reinterpret_cast<uint4*>(dst + 8 * v1) = u1;
+      } else {
+        store8(dst + 8 * v0, x0);
+        store8(dst + 8 * v1, x1);
+      }
+    }
   }
 }
 
@@ -184,14 +273,36 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float* table, int rows,
 
 }  // namespace
 
+namespace {
+// warps of a launch at one token each from which four tokens per warp pay: four waves of them
+constexpr long long kManyWarps = 4LL * 148 * 32;
+
+template <int D, int kTokens, bool CACHED, bool FP8>
+cudaError_t run_norm_rope(const NormRopeLaunch& a, int head_groups, cudaStream_t stream) {
+  const long long token_groups = ((long long)a.B * a.T + kTokens - 1) / kTokens;
+  // warps per CTA: the head groups in the fewest CTAs of at most eight, evenly
+  const int head_blocks = (head_groups + 7) / 8, warps = (head_groups + head_blocks - 1) / head_blocks;
+  if (token_groups * head_blocks > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_beside(norm_rope_kernel<D, kTokens, CACHED, FP8>, dim3((unsigned)(token_groups * head_blocks)),
+                       32 * warps, 0, stream, true, a, head_blocks);
+}
+
+template <int D, bool CACHED, bool FP8>
+cudaError_t run_norm_rope(const NormRopeLaunch& a, cudaStream_t stream) {
+  const int heads = 32 / (D / 16), groups = (a.Hq + a.Hkv * (CACHED ? 2 : 1) + heads - 1) / heads;
+  return (long long)a.B * a.T * groups >= kManyWarps ? run_norm_rope<D, 4, CACHED, FP8>(a, groups, stream)
+                                                     : run_norm_rope<D, 1, CACHED, FP8>(a, groups, stream);
+}
+
+template <int D>
+cudaError_t run_norm_rope(const NormRopeLaunch& a, cudaStream_t stream) {
+  if (!a.cached) return run_norm_rope<D, false, false>(a, stream);
+  return a.fp8 ? run_norm_rope<D, true, true>(a, stream) : run_norm_rope<D, true, false>(a, stream);
+}
+}  // namespace
+
 cudaError_t launch_norm_rope(const NormRopeLaunch& a, cudaStream_t stream) {
-  const long long rows = (long long)a.B * a.T * (a.Hq + a.Hkv * (a.cached ? 2 : 1));
-  const int per_block = 256 / (a.d / 16);
-  const long long blocks = (rows + per_block - 1) / per_block;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  if (a.d == 128) norm_rope_kernel<128><<<(unsigned)blocks, 256, 0, stream>>>(a);
-  else norm_rope_kernel<64><<<(unsigned)blocks, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return a.d == 128 ? run_norm_rope<128>(a, stream) : run_norm_rope<64>(a, stream);
 }
 
 cudaError_t launch_rope_table(float* table, int rows, int rot, double theta, cudaStream_t stream) {

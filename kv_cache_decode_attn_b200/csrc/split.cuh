@@ -346,30 +346,12 @@ __device__ __forceinline__ bool consumers_abort(const volatile int* abort_flag) 
   return r != 0;
 }
 
-// Launch a kernel; `beside`: without waiting for the one before it in the stream.
-template <class Kernel, class... Args>
-inline cudaError_t launch_beside(Kernel kern, dim3 grid, int threads, int smem, cudaStream_t stream, bool beside,
-                                 const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = beside ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 // Launch a SEL instance of a warp-level kernel, with one CTA more if p.fence.
 template <class Kernel>
 inline cudaError_t launch_sel(Kernel kern, int threads, int smem, const CUtensorMap& tk, const CUtensorMap& tv,
                               const SplitParams& sp, int B, cudaStream_t stream) {
   const dim3 grid = sp.stream ? dim3(sp.stream * sp.Hkv + sp.fence) : dim3(sp.max_chunks + sp.fence, sp.Hkv, B);
-  return launch_beside(kern, grid, threads, smem, stream, sp.fence != 0, tk, tv, sp);
+  return launch_beside(kern, grid, threads, smem, stream, true, tk, tv, sp);
 }
 
 // FP8 caches, at most 8 query rows per KV head: the transposed-product split kernel (decode_fp8.cu)
