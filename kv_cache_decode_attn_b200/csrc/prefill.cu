@@ -42,11 +42,14 @@
 //
 // Sliding window with a few first tokens (WIN instances, causal): the query at
 // position p sees keys j <= p with j > p - window or j < sinks.  Each item numbers
-// the keys its 256 rows can see consecutively, in 16-token blocks: the first
-// tokens' blocks, then the blocks from the first row's window on (the gap between
-// them, whole blocks, is skipped), so an item's work is about window + 256 keys
-// whatever its position.  Every K/V tile is eight 16-row boxes in any layout; masks
-// and limits work on the numbers.
+// the keys its 256 rows can see: the first tokens, padded to whole 128-key tiles, then
+// the keys from its first row's window on (rounded down to a 16-token block), so a tile
+// is one run of positions, an item's work is about window + 256 keys whatever its
+// position, and masks and limits work on the numbers.  Query tile B leaves out the
+// window tiles that only tile A's rows see.  With up to 64 first tokens their tile is a
+// narrow one: MMAs and softmax over just those columns.  4096-token prompts with a window
+// of 1024 and 4 first tokens: 11 and 10 tiles per item of two query tiles without the
+// last two points, 9 and a narrow one each with them.
 //
 // Online softmax (running maximum m and denominator l per row, base-2 exponent
 // with the scale folded in): a row's reference maximum is only raised when the
@@ -89,6 +92,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;   // log2 of the largest allowed p
 constexpr int kMaxStages = 4;     // K or V ring stages (barrier slots)
+constexpr int kNarrow = 64;       // WIN: widest narrow tile of first tokens
 constexpr int kItemSlots = 4;     // work items published ahead (see item_slot)
 
 // K/V ring depth.  d = 128: two stages (a third K stage measured no faster: the copies
@@ -195,9 +199,10 @@ struct Item {
   int qb, h, b, n_kv0, n_load;   // n_kv0: K/V tiles of query tile A; n_load: of tile B (>= n_kv0)
   int L, off;                    // keys of the sequence; query row i sees keys j <= off + i (causal)
   bool bad;                      // invalid length (cached forms): the rows are written as NaN
-  // WIN: L and off count the item's selected keys; number v is position v below s16 and
-  // v + gap from there on
-  int s16, gap;
+  // WIN: L and off count the item's numbered keys; the tiles below s_tiles hold the first
+  // tokens, a number v from there on is position v + gap; query tile B's rows see the tiles
+  // below s_tiles and from jb on; cols < kBN: the first tile is narrow
+  int s_tiles, gap, w0, jb, cols;   // w0: first position read past the first tokens
 };
 
 // Work item w.  Dense with short sequences: heaviest causal query blocks first, then
@@ -226,7 +231,8 @@ __device__ __forceinline__ Item item_of(int w, const PrefillParams& p, const int
     it.qb = p.n_qblocks - 1 - rem2 / p.G;
     it.h = kvh * p.G + rem2 % p.G;
   }
-  it.s16 = it.gap = 0;
+  it.s_tiles = it.gap = it.w0 = it.jb = 0;
+  it.cols = kBN;
   if constexpr (WIN) {
     int L = p.N;
     it.bad = false;
@@ -235,15 +241,19 @@ __device__ __forceinline__ Item item_of(int w, const PrefillParams& p, const int
       it.bad = L < p.N || L > p.max_keys;
       if (it.bad) L = p.N;             // a safe stand-in; the host checked p.N <= p.max_keys
     }
-    it.s16 = (p.sinks + kPageTokens - 1) & ~(kPageTokens - 1);
-    // block of the first key in the window of the item's first row
-    const int w0 = max(0, L - p.N + 2 * it.qb * kBM - p.window + 1) & ~(kPageTokens - 1);
-    it.gap = max(0, w0 - it.s16);
+    it.s_tiles = (p.sinks + kBN - 1) / kBN;
+    const int row0 = L - p.N + 2 * it.qb * kBM;   // position of the item's first row
+    // block of the first key in that row's window
+    it.w0 = max(0, row0 - p.window + 1) & ~(kPageTokens - 1);
+    it.gap = max(0, it.w0 - it.s_tiles * kBN);
     it.L = L - it.gap;
     it.off = it.L - p.N;
     const int nt = (it.L + kBN - 1) / kBN;
     it.n_kv0 = min((it.off + 2 * it.qb * kBM + kBM + kBN - 1) / kBN, nt);
     it.n_load = min((it.off + 2 * it.qb * kBM + 2 * kBM + kBN - 1) / kBN, nt);
+    it.jb = min(max(max(0, row0 + kBM - p.window + 1 - it.gap) / kBN, it.s_tiles), it.n_load - 1);
+    const int s16 = (p.sinks + kPageTokens - 1) & ~(kPageTokens - 1);
+    if (it.gap > 0 && s16 > 0 && s16 <= kNarrow) it.cols = s16;
   } else if constexpr (kDenseKv<KV>) {
     it.L = p.N;
     it.off = 0;
@@ -293,6 +303,9 @@ __device__ __forceinline__ float2 exp2_fma2(float2 x) {
 // FMA pipe gained 3-4 % on the GPT-2-sized prefill.
 template <int D>
 constexpr unsigned exp_fma_pairs() { return D == 64 ? 0x92u : 0u; }
+
+// the lowest n bits (all for n >= 32, none for n <= 0)
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u); }
 
 // Exponentials of keys 64*HALF .. 64*HALF+63 of one row: p = 2^(s*sc - m) (nm = -m), the
 // pair sums added to sum2, and bf16 P stored to TMEM at taddr (two keys per column).
@@ -461,16 +474,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         itm = item_of<KV, WIN>(wi, p, order);
       }
       const int kvh = itm.h / p.G;
-      // WIN: position of the first key of this lane's 16-token block of tile t
-      auto block_pos = [&](int t) -> int {
+      // WIN: position of the first key of tile t
+      auto tile_pos = [&](int t) -> int { return t * kBN + (WIN && t >= itm.s_tiles ? itm.gap : 0); };
+      // paged: whether this lane's 16-token block of tile t (lanes >= 8: none) holds keys some row
+      // may see, and the physical block
+      auto needs = [&](int t) -> bool {
         const int vt = t * kBN + lane * kPageTokens;
-        return vt + (vt >= itm.s16 ? itm.gap : 0);
+        return lane < kBlocks && vt < itm.L && (!WIN || vt < p.sinks || tile_pos(t) + lane * kPageTokens >= itm.w0);
       };
-      // paged: this lane's physical block of tile t (lanes >= 8 and blocks past L: none)
       auto read_id = [&](int t) -> int {
-        const int nb = min(kBlocks, (itm.L - t * kBN + kPageTokens - 1) / kPageTokens);
-        const int at = WIN ? block_pos(t) / kPageTokens : t * kBlocks + lane;
-        return lane < nb ? __ldg(p.page_table + (size_t)itm.b * p.max_blocks + at) : -1;
+        return needs(t) ? __ldg(p.page_table + (size_t)itm.b * p.max_blocks + tile_pos(t) / kPageTokens + lane) : -1;
       };
       int id = 0;
       if constexpr (KV == KV_PAGED) id = read_id(0);
@@ -482,34 +495,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         last[s] = g;
         uint8_t* const dst = ring + s * C::kTileBytes;
-        if constexpr (WIN && KV != KV_PAGED) {
-          const int nb = min(kBlocks, (itm.L - t * kBN + kPageTokens - 1) / kPageTokens);
-          if (lane == 0) mbar_arrive_expect_tx(&bars[full0 + s], nb * C::kHalves * kPageTokens * 128);
-          __syncwarp();
-          if (lane < nb) {
-#pragma unroll
-            for (int hh = 0; hh < C::kHalves; ++hh)
-              tma_load_4d(dst + hh * C::kHalfBytes + lane * kPageTokens * 128, map, &bars[full0 + s], hh * 64, kvh,
-                          block_pos(t), itm.b, keep);
-          }
-        } else if constexpr (KV != KV_PAGED) {
+        if constexpr (KV != KV_PAGED) {
           if (lane == 0) {
             mbar_arrive_expect_tx(&bars[full0 + s], C::kTileBytes);
 #pragma unroll
             for (int hh = 0; hh < C::kHalves; ++hh)
-              tma_load_4d(dst + hh * C::kHalfBytes, map, &bars[full0 + s], hh * 64, kvh, t * kBN, itm.b, keep);
+              tma_load_4d(dst + hh * C::kHalfBytes, map, &bars[full0 + s], hh * 64, kvh, tile_pos(t), itm.b, keep);
           }
         } else {
           // one 16-row box per 64 columns of d and physical block holding keys of this tile below L
-          const int nb = min(kBlocks, (itm.L - t * kBN + kPageTokens - 1) / kPageTokens);
+          const bool need = needs(t);
+          const int nb = __popc(__ballot_sync(0xffffffffu, need));
           int blk = id;
-          if (lane < nb && (blk < 0 || blk >= p.num_blocks)) {
+          if (need && (blk < 0 || blk >= p.num_blocks)) {
             atomicOr(p.status, DEV_PAGE_ID);
             blk = 0;   // keep the byte count; the result is flagged invalid
           }
           if (lane == 0) mbar_arrive_expect_tx(&bars[full0 + s], nb * C::kHalves * kPageTokens * 128);
           __syncwarp();
-          if (lane < nb) {
+          if (need) {
 #pragma unroll
             for (int hh = 0; hh < C::kHalves; ++hh)
               tma_load_3d(dst + hh * C::kHalfBytes + lane * kPageTokens * 128, map, &bars[full0 + s], hh * 64, kvh,
@@ -537,7 +541,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // of tensor-core time.
     const uint32_t leader = elect_one();
     constexpr int kKStages = C::kKStages, kVStages = C::kVStages;
-    constexpr uint32_t idS = idesc_bf16(kBM, kBN, 0, 0);     // Q (K-major) x K^T (K-major)
     constexpr uint32_t idO = idesc_bf16(kBM, D, 0, 1);       // P (TMEM) x V (N-major)
     // shared-memory descriptors (128-byte swizzle, 1024-byte row-group stride): only the
     // low word varies -- the start address in 16-byte units -- so every operand is a
@@ -547,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t k_lo0 = desc_lo(sbase + C::kKOff, 16);
     const uint32_t v_lo0 = desc_lo(sbase + C::kVOff, C::kHalfBytes);
     constexpr uint32_t kStageLo = C::kTileBytes >> 4;     // one ring stage in descriptor units
-    auto issue_s = [&](int t, int ks) {     // S_t = Q_t K^T, K in ring stage ks
+    auto issue_s = [&](int t, int ks, uint32_t idS = idesc_bf16(kBM, kBN, 0, 0)) {   // S_t = Q_t K^T, K in ring stage ks
       const uint32_t qa = t ? q_lo1 : q_lo0, kb = k_lo0 + ks * kStageLo;
       const uint32_t d = tmem + C::s_col(t);
       tc_mma_ss_lo<0>(leader, d, qa, kb, idS);
@@ -572,15 +575,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     int pcnt[2] = {0, 0};                  // P phases consumed per tile
     // both halves of PV_t(j): the first as soon as the softmax group has published P of
     // the first 64 keys (the second half's exponentials overlap it)
-    auto pv_tile = [&](int t, int st, int j, int it) -> bool {
+    auto pv_tile = [&](int t, int st, bool first, int it) -> bool {
       const uint32_t par = (pcnt[t]++) & 1;
       if (!wait_or_abort(&bars[B_PHALF + t], par, abort_flag, p.status)) return false;
-      if (j == 0 && it > 0 && !wait_or_abort(&bars[B_OFREE + t], (it - 1) & 1, abort_flag, p.status)) return false;
+      if (first && it > 0 && !wait_or_abort(&bars[B_OFREE + t], (it - 1) & 1, abort_flag, p.status)) return false;
       tc_fence_after();
-      issue_pv(t, st, j == 0, 0);
+      issue_pv(t, st, first, 0);
       if (!wait_or_abort(&bars[B_PFULL + t], par, abort_flag, p.status)) return false;
       tc_fence_after();
-      issue_pv(t, st, j == 0, 1);
+      issue_pv(t, st, first, 1);
+      return true;
+    };
+    // WIN: PV_t of an item's narrow first tile (cols keys, published at once)
+    auto pv_narrow = [&](int t, int vs, int cols, int it) -> bool {
+      const uint32_t par = (pcnt[t]++) & 1;
+      if (!wait_or_abort(&bars[B_PHALF + t], par, abort_flag, p.status)) return false;
+      if (it > 0 && !wait_or_abort(&bars[B_OFREE + t], (it - 1) & 1, abort_flag, p.status)) return false;
+      if (!wait_or_abort(&bars[B_PFULL + t], par, abort_flag, p.status)) return false;
+      tc_fence_after();
+      const uint32_t vb = v_lo0 + vs * kStageLo, d = tmem + C::o_col(t), pa = tmem + C::s_col(t);
+      tc_mma_ts_lo<0>(leader, d, pa, vb, idO);
+      for (int kk = 1; kk < cols / 16; ++kk) tc_mma_ts_lo<1>(leader, d, pa + kk * 8, vb + ((kk * 16 * 128) >> 4), idO);
       return true;
     };
     int g = 0, it = 0;                     // K/V tiles consumed, items done
@@ -592,13 +607,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item itm = item_of<KV, WIN>(w, p, order);
       const int n_load = __shfl_sync(0xffffffffu, itm.n_load, 0);
       const int n_kv0 = __shfl_sync(0xffffffffu, itm.n_kv0, 0);
+      // WIN: whether query tile B has rows that see tile j
+      const int s_tiles = WIN ? __shfl_sync(0xffffffffu, itm.s_tiles, 0) : 0;
+      const int jb = WIN ? __shfl_sync(0xffffffffu, itm.jb, 0) : 0;
+      const int cols = WIN ? __shfl_sync(0xffffffffu, itm.cols, 0) : kBN;
+      auto sees_b = [&](int j) { return !WIN || j < s_tiles || j >= jb; };
+      const int n_keys = WIN ? __shfl_sync(0xffffffffu, itm.L, 0) : 0;
+      const int dead_end = WIN ? __shfl_sync(0xffffffffu, itm.off + 2 * itm.qb * kBM, 0) + 1 - p.window : 0;
+      bool first_b = true;
       const int g0 = g;
       const int ks0 = g0 % kKStages;
       ok = wait_or_abort(&bars[B_KFULL + ks0], (g0 / kKStages) & 1, abort_flag, p.status);
       if (!ok) break;
       tc_fence_after();
-      issue_s(0, ks0);
-      issue_s(1, ks0);
+      if constexpr (WIN) {
+        const uint32_t id = idesc_bf16(kBM, cols, 0, 0);
+        issue_s(0, ks0, id);
+        if (sees_b(0)) issue_s(1, ks0, id);
+      } else {
+        issue_s(0, ks0);
+        issue_s(1, ks0);
+      }
       tc_commit_if(leader, &bars[B_KEMPTY + ks0]);
       for (int j = 0; j < n_load; ++j) {
         const int gj = g0 + j, st = gj % kVStages;
@@ -610,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // V rows of keys >= L: any bytes (cache) or never loaded (paged); the PV MMAs
           // would multiply them by p = 0.  Zeroed here, by the warp that consumes the V
           // phases in order, before either PV of the tile is issued.
-          const int valid = __shfl_sync(0xffffffffu, itm.L, 0) - j * kBN;
+          const int valid = (WIN ? n_keys : __shfl_sync(0xffffffffu, itm.L, 0)) - j * kBN;
           if (valid < kBN) {
             uint8_t* vst = smem + C::kVOff + st * C::kTileBytes;
             for (int idx = max(valid, 0) * 8 + lane; idx < kBN * 8; idx += 32)
@@ -624,8 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (WIN) {
           // keys that no row of the item sees (between `sinks` and the first row's window)
           // may hold anything too
-          const int z0 = max(p.sinks - j * kBN, 0);
-          const int z1 = min(__shfl_sync(0xffffffffu, itm.off + 2 * itm.qb * kBM, 0) + 1 - p.window - j * kBN, kBN);
+          const int z0 = max(p.sinks - j * kBN, 0), z1 = min(dead_end - j * kBN, kBN);
           if (z0 < z1) {
             uint8_t* vst = smem + C::kVOff + st * C::kTileBytes;
             for (int idx = z0 * 8 + lane; idx < z1 * 8; idx += 32)
@@ -637,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (j < n_kv0) {
-          ok = pv_tile(0, st, j, it);
+          ok = WIN && j == 0 && cols < kBN ? pv_narrow(0, st, cols, it) : pv_tile(0, st, j == 0, it);
           if (!ok) break;
           if (j == n_kv0 - 1) tc_commit_if(leader, &bars[B_ODONE + 0]);
         }
@@ -647,12 +675,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (j + 1 < n_kv0) issue_s(0, ksn);
         }
-        ok = pv_tile(1, st, j, it);
-        if (!ok) break;
+        if (sees_b(j)) {
+          ok = WIN && j == 0 && cols < kBN ? pv_narrow(1, st, cols, it) : pv_tile(1, st, first_b, it);
+          if (!ok) break;
+          first_b = false;
+        }
         tc_commit_if(leader, &bars[B_VEMPTY + st]);        // V of this stage is no longer needed
         if (j == n_load - 1) tc_commit_if(leader, &bars[B_ODONE + 1]);
         if (next_k) {
-          issue_s(1, ksn);
+          if (sees_b(j + 1)) issue_s(1, ksn);
           tc_commit_if(leader, &bars[B_KEMPTY + ksn]);
           // that was the item's last MMA reading Q: the next item's Q may land once it is done
           if (j + 2 == n_load) tc_commit_if(leader, &bars[B_QEMPTY]);
@@ -683,9 +714,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q_row = (2 * itm.qb + t) * kBM + row;
     const int nkv = t ? itm.n_load : itm.n_kv0;
     float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < nkv; ++j) {
+    const int j_first = WIN && t == 1 && itm.s_tiles == 0 ? itm.jb : 0;   // the group's first tile
+    for (int j = j_first; j < nkv; ++j) {
+      if (WIN && t == 1 && j == itm.s_tiles) j = itm.jb;                  // tiles that none of its rows sees
       if (!wait_or_abort(&bars[B_SFULL + t], (scnt++) & 1, abort_flag, p.status)) { ok = false; break; }
       tc_fence_after();
+      if constexpr (WIN) {
+        if (j == 0 && itm.cols < kBN) {
+          // narrow tile: the first tokens, which every row sees
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < itm.cols; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(s_addr + c, r);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c + e < p.sinks) mx = fmaxf(mx, __uint_as_float(r[e]));
+          }
+          m = mx * p.scale_log2;
+#pragma unroll 1
+          for (int c = 0; c < itm.cols; c += 16) {   // P of these columns lies below S of the next
+            uint32_t r[16], pk[8];
+            tmem_ld16(s_addr + c, r);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float p0 = c + e < p.sinks ? ex2(fmaf(__uint_as_float(r[e]), p.scale_log2, -m)) : 0.f;
+              const float p1 = c + e + 1 < p.sinks ? ex2(fmaf(__uint_as_float(r[e + 1]), p.scale_log2, -m)) : 0.f;
+              l += p0 + p1;
+              pk[e / 2] = pack_bf16x2(p0, p1);
+            }
+            tmem_st8(s_addr + c / 2, pk);
+          }
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bars[B_PHALF + t]);
+            mbar_arrive(&bars[B_PFULL + t]);
+          }
+          continue;
+        }
+      }
       float s[kBN];
 #pragma unroll
       for (int c = 0; c < kBN; c += 32) {
@@ -699,19 +770,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       // mask (causal diagonal tile, or keys past N) and the row maximum of the raw scores
       const int key0 = j * kBN;
       const int lim = p.causal ? min(itm.off + q_row - key0 + 1, itm.L - key0) : (itm.L - key0);   // visible: [0, lim)
-      if (lim < kBN) {
+      bool masked = lim < kBN;
+      if constexpr (WIN) {
+        // not seen either: keys from `sinks` to the row's window; one bit per key
+        const int z0 = max(p.sinks - key0, 0), z1 = min(itm.off + q_row + 1 - p.window - key0, kBN);
+        masked = masked || z0 < z1;
+        if (masked) {
+#pragma unroll
+          for (int w = 0; w < kBN / 32; ++w) {
+            const uint32_t seen = low_bits(lim - 32 * w) & (low_bits(z0 - 32 * w) | ~low_bits(max(z0, z1) - 32 * w));
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[32 * w + c] = (seen >> c & 1u) ? s[32 * w + c] : -INFINITY;
+          }
+        }
+      } else if (masked) {
 #pragma unroll
         for (int c = 0; c < kBN; ++c) s[c] = (c < lim) ? s[c] : -INFINITY;
-      }
-      bool gap_masked = false;
-      if constexpr (WIN) {
-        // not seen either: keys from `sinks` to the row's window
-        const int z0 = max(p.sinks - key0, 0), z1 = min(itm.off + q_row + 1 - p.window - key0, kBN);
-        if (z0 < z1) {
-          gap_masked = true;
-#pragma unroll
-          for (int c = 0; c < kBN; ++c) s[c] = (c >= z0 && c < z1) ? -INFINITY : s[c];
-        }
       }
       float mx8[8];
 #pragma unroll
@@ -737,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // O_t is stable here (PV_t(j-1) completed before S_t(j) did) and PV_t(j)
       // waits for this group's first arrival below
       // (16 columns at a time: the scores still occupy 128 registers)
-      if (warp_raise && j > 0) {
+      if (warp_raise && j > j_first) {
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           uint32_t r[16];
@@ -754,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       // rows with masked keys (-inf scores) take every exponential on the SFU
       constexpr unsigned kFma = exp_fma_pairs<D>();
-      const bool soft = kFma != 0 && !__any_sync(0xffffffffu, lim < kBN || (WIN && gap_masked));
+      const bool soft = kFma != 0 && !__any_sync(0xffffffffu, masked);
       if (soft) exp_store_half<0, true, kFma>(s, sc2, nm2, sum2, s_addr);
       else exp_store_half<0, false, kFma>(s, sc2, nm2, sum2, s_addr);
       tc_wait_st();
@@ -864,20 +938,18 @@ template <int D, int KV, bool WIN = false>
 cudaError_t run_prefill(const PrefillLaunch& a, cudaStream_t stream) {
   using C = PrefillCfg<D>;
   CUtensorMap tq, tk, tv;
-  // 4-D views {d, heads, rows, B}; box {64, 1, rows of one copy, 1} with the 128-byte swizzle
-  constexpr int kKvRows = WIN ? kPageTokens : kBN;
-  auto enc = [&](CUtensorMap* m, const void* base, int heads, int rows, int box_rows) {
+  // 4-D views {d, heads, rows, B}; box {64, 1, 128, 1} with the 128-byte swizzle
+  auto enc = [&](CUtensorMap* m, const void* base, int heads, int rows) {
     cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)a.B};
     cuuint64_t str[3] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2, (cuuint64_t)rows * heads * D * 2};
-    cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
+    cuuint32_t box[4] = {64, 1, (cuuint32_t)kBN, 1};
     return encode_tmap_nd(m, base, 4, dims, str, box);
   };
-  if (enc(&tq, a.q, a.Hq, a.N, kBM)) return cudaErrorInvalidValue;
+  if (enc(&tq, a.q, a.Hq, a.N)) return cudaErrorInvalidValue;
   if constexpr (kDenseKv<KV>) {
-    if (enc(&tk, a.k, a.Hkv, a.N, kKvRows) || enc(&tv, a.v, a.Hkv, a.N, kKvRows)) return cudaErrorInvalidValue;
+    if (enc(&tk, a.k, a.Hkv, a.N) || enc(&tv, a.v, a.Hkv, a.N)) return cudaErrorInvalidValue;
   } else if constexpr (KV == KV_CACHE) {
-    if (enc(&tk, a.k, a.Hkv, a.capacity, kKvRows) || enc(&tv, a.v, a.Hkv, a.capacity, kKvRows))
-      return cudaErrorInvalidValue;
+    if (enc(&tk, a.k, a.Hkv, a.capacity) || enc(&tv, a.v, a.Hkv, a.capacity)) return cudaErrorInvalidValue;
   } else {
     // pools [num_blocks, 16, Hkv, d] as {d, Hkv, num_blocks * 16}; one 16-row box per block
     const uint64_t rows = (uint64_t)a.num_blocks * kPageTokens;
