@@ -957,8 +957,10 @@ int prefix_chunk_tokens(int tokens, int G, int Hkv, int prefix, int num_splits, 
   if (num_splits > 0 || !decode_uses_tc(G * tokens, fp8))
     return decode_chunk_tokens(1, tokens, G, Hkv, prefix, num_splits, fp8);
   const long long units = (long long)Hkv * decode_row_tiles(tokens, G);
-  const long long items = device_sms();
-  const long long chunk = std::max((prefix * units + items - 1) / items, 128LL);
+  // one wave of CTAs: with 64 sequences of 4 heads behind 32K tokens (two row tiles of 8 KV
+  // heads), 18 chunks; at 128 chunks their partials alone were 134 MB
+  const long long chunks = std::max(kDecodeTcCtasPerSm * device_sms() / units, 1LL);
+  const long long chunk = std::max((prefix + chunks - 1) / chunks, 128LL);
   return (int)((chunk + kDecodeTcTile - 1) / kDecodeTcTile * kDecodeTcTile);
 }
 
@@ -968,9 +970,9 @@ int decode_balanced_chunks(int B, int Hkv, int items_per_slot) {
   return n > B ? n : B;
 }
 
-int decode_stream_ctas(int B, int R, int Hkv, int max_keys, bool fp8, int per_sm) {
+int decode_stream_ctas(int B, int R, int Hkv, int max_keys, bool fp8) {
   if (B > kStreamMaxB || (long long)B * ((max_keys + kDecodeTile - 1) / kDecodeTile) > INT32_MAX) return 0;
-  if (per_sm == 0) per_sm = fp8 ? (R <= 8 ? 3 : (R <= 16 ? 2 : 1)) : 2;
+  const int per_sm = fp8 ? (R <= 8 ? 3 : (R <= 16 ? 2 : 1)) : 2;   // resident CTAs of the kernel
   return std::max(per_sm * device_sms() / Hkv, 1);
 }
 

@@ -79,7 +79,7 @@ struct TcCfg {
   static constexpr int kRawVOff = kRawKOff + (FP8 ? kStages * kRawBytes : 0);
   static constexpr int kBarOff = kRawVOff + (FP8 ? kStages * kRawBytes : 0);
   static constexpr int kPlanOff = kBarOff + 256;             // balanced split: the plan, built per CTA
-  static constexpr int kPlanBytes = kBalancedMaxB * 4 * 4;   // length, base share, chunks, first chunk
+  static constexpr int kPlanBytes = kBalancedMaxB * (4 * 4 + 8);   // length, base share, chunks, first chunk; remainder
   static constexpr int kSmemBytes = kPlanOff + kPlanBytes + 1024;
   static constexpr int kSCols = kTok;                        // one S buffer (fp32 scores of a tile)
   static constexpr int kOCol = 2 * kSCols;                   // S0 | S1 | O
@@ -151,6 +151,7 @@ __device__ __forceinline__ BalancedItem balanced_item(const TcParams& p, int* pl
   int* base = plan_smem + kBalancedMaxB;                  // [B] floor share
   int* nb = plan_smem + 2 * kBalancedMaxB;                // [B] chunks
   int* first = plan_smem + 3 * kBalancedMaxB;             // [B] first chunk
+  long long* part = reinterpret_cast<long long*>(plan_smem + 4 * kBalancedMaxB);   // [B] remainders
   const int B = p.B, N = p.n_chunks;
   for (int i = threadIdx.x; i < B; i += blockDim.x) {
     if constexpr (SEL) {
@@ -164,18 +165,19 @@ __device__ __forceinline__ BalancedItem balanced_item(const TcParams& p, int* pl
   long long tot = 0;
   for (int i = 0; i < B; ++i) tot += len[i];
   const long long spare = N - B;
-  for (int i = threadIdx.x; i < B; i += blockDim.x) base[i] = (int)((long long)len[i] * spare / tot);
+  for (int i = threadIdx.x; i < B; i += blockDim.x) {
+    const long long share = (long long)len[i] * spare;
+    base[i] = (int)(share / tot);
+    part[i] = share - base[i] * tot;
+  }
   __syncthreads();
   long long used = 0;
   for (int i = 0; i < B; ++i) used += base[i];
   const long long extra = spare - used;                   // 0 <= extra < B
   for (int i = threadIdx.x; i < B; i += blockDim.x) {
-    const long long ri = (long long)len[i] * spare % tot;
+    const long long ri = part[i];
     int rank = 0;
-    for (int j = 0; j < B; ++j) {
-      const long long rj = (long long)len[j] * spare % tot;
-      rank += (rj > ri) || (rj == ri && j < i);
-    }
+    for (int j = 0; j < B; ++j) rank += (part[j] > ri) || (part[j] == ri && j < i);
     nb[i] = 1 + base[i] + (rank < extra ? 1 : 0);
   }
   __syncthreads();
@@ -270,12 +272,26 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
   int c, rt, g, b, chunk;
   size_t item;
   if constexpr (SEL) {
-    if (!p.fence) grid_dependency_wait();   // launched early too; with p.fence the kernel before has waited
-    if (p.early) launch_dependents();
     if (p.fence && blockIdx.x == gridDim.x - 1) {
       if (blockIdx.y == 0 && blockIdx.z == 0) grid_dependency_wait();
       return;
     }
+  }
+  // TMEM first of all: a second CTA of the SM starts only once this one has given up its
+  // right to allocate (measured: 4.4 us after the first when that followed the plan)
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  auto leave = [&] {   // the whole CTA, which has nothing to do
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(*tmem_slot, C::kTmemCols);
+  };
+  if constexpr (SEL) {
+    if (!p.fence) grid_dependency_wait();   // launched early too; with p.fence the kernel before has waited
+    if (p.early) launch_dependents();
   }
   if (p.balanced) {
     const BalancedItem bi = balanced_item<SEL, PAGED>(p, reinterpret_cast<int*>(smem + C::kPlanOff));
@@ -298,10 +314,14 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
   // invalid lengths: their rows are made NaN by the combine kernel
   if (sk.bad) {
     if (SEL && threadIdx.x == 0) atomicOr(p.status, DEV_SEQLEN);
+    leave();
     return;
   }
   const int tok_begin = c * chunk;
-  if (tok_begin >= L) return;   // the combine reads only chunks that start before L
+  if (tok_begin >= L) {   // the combine reads only chunks that start before L
+    leave();
+    return;
+  }
   const int t0 = rt * p.TT;                      // first token of this row tile
   const int tile_tokens = min(p.TT, p.T - t0);
   const int tile_rows = tile_tokens * p.G;       // live rows: 0 .. tile_rows - 1
@@ -312,6 +332,7 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
     // no key of this chunk is visible to any row of the tile: an empty partial
     for (int i = threadIdx.x; i < tile_rows * D; i += blockDim.x) p.part_o[row0 * D + i] = 0.f;
     for (int r = threadIdx.x; r < tile_rows; r += blockDim.x) p.part_lse[row0 + r] = -INFINITY;
+    leave();
     return;
   }
   const int n_tiles = (tok_end - tok_begin + kTok - 1) / kTok;
@@ -334,6 +355,7 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
       // barrier (the scales are uniform across it)
       if (threadIdx.x == 0 && c == 0 && rt == 0) atomicOr(p.status, DEV_SCALE);
       for (int r = threadIdx.x; r < tile_rows; r += blockDim.x) p.part_lse[row0 + r] = NAN;
+      leave();
       return;
     }
   }
@@ -377,10 +399,6 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
     }
   }
   fence_proxy_async_smem();
-  if (warp == 0) {
-    tmem_alloc(tmem_slot, C::kTmemCols);
-    tmem_relinquish();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

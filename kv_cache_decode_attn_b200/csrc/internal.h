@@ -49,8 +49,8 @@ int decode_balanced_chunks(int B, int Hkv, int items_per_slot = kBalancedItemsPe
 
 // Windowed and shared-prefix decode (the SEL instances) on the warp-level kernels, automatic
 // splitting: this many CTAs per KV head share its tiles evenly (0: too many sequences or tiles for it,
-// one CTA per chunk then).  per_sm > 0 sets the CTAs per SM, else as many as are resident.
-int decode_stream_ctas(int B, int R, int Hkv, int max_keys, bool fp8, int per_sm = 0);
+// one CTA per chunk then).
+int decode_stream_ctas(int B, int R, int Hkv, int max_keys, bool fp8);
 
 // One CTA whose thread waits on an mbarrier nothing arrives at (bounded like every
 // wait of the library) and then sets DEV_TIMEOUT (csrc/selftest.cu).
