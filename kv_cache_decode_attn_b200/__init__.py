@@ -2,7 +2,8 @@
 
 Python binding of ``libkvattn.so``: the functions below carry the C-ABI names of
 ``include/attn.h`` and only marshal arguments (device pointers, sizes, the
-current CUDA stream) from torch tensors.  Every step of the computation runs in
+current CUDA stream) from torch tensors, the newer ones in a compiled module
+(``binding/marshal.cpp``).  Every step of the computation runs in
 the library's CUDA kernels; there is no CPU or library fallback, and importing
 this package fails if the library has not been built
 (``python kv_cache_decode_attn_b200/build.py``).
@@ -114,6 +115,10 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+try:
+    from . import _marshal  # noqa: E402
+except ImportError as e:
+    raise ImportError(f"{e}: build the package with `python kv_cache_decode_attn_b200/build.py`") from e
 
 
 class AttnError(RuntimeError):
@@ -169,54 +174,14 @@ def _int32(n) -> int:
     return n
 
 
-def _current(t, name) -> int:
-    """The current device, which the calls run on and ``t`` has to be on."""
+def _here(t, stream):
+    """The current device, which the calls run on and ``t`` has to be on, and the stream's handle."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+        raise ValueError("the calls take CUDA tensors")
     dev = torch.cuda.current_device()
     if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    return dev
-
-
-def _at(t, name, dtype, dev):
-    """Pointer of a contiguous tensor of device ``dev`` (None stays None)."""
-    if t is None:
-        return None
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, like the other tensors")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    return t.data_ptr()
-
-
-def _cache_fits(k_cache, v_cache, page_table, lens, B, d):
-    """The cache, page table and lengths belong to B sequences of head size d; the geometry."""
-    n, cap, Hkv, dc = k_cache.shape
-    if v_cache.shape != k_cache.shape or dc != d or lens.shape != (B,):
-        raise ValueError("shape mismatch")
-    if page_table is None:
-        if n != B:
-            raise ValueError("a contiguous cache must be [B, capacity, Hkv, d]")
-        return 0, 0, cap, Hkv
-    if cap != 16 or page_table.shape[0] != B:
-        raise ValueError("a paged cache must be [num_blocks, 16, Hkv, d] with a page table [B, max_blocks]")
-    return page_table.shape[1], n, 0, Hkv
-
-
-def _caches(k_cache, v_cache, scales, Hkv, dev):
-    """Pointers of a bf16 cache (scales None), or of an FP8 cache and of its scales."""
-    if scales is None:
-        return (_at(k_cache, "k_cache", torch.bfloat16, dev), _at(v_cache, "v_cache", torch.bfloat16, dev)), ()
-    ks, vs = scales
-    if ks.shape != (Hkv,) or vs.shape != (Hkv,):
-        raise ValueError("k_scale and v_scale must be [Hkv]")
-    if k_cache.get_device() != dev or v_cache.get_device() != dev:
-        raise ValueError(f"the caches must be on cuda:{dev}, like the other tensors")
-    return ((_codes(k_cache, "k_cache"), _codes(v_cache, "v_cache")),
-            (_at(ks, "k_scale", torch.float32, dev), _at(vs, "v_scale", torch.float32, dev)))
+        raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+    return dev, (_raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream))
 
 
 def attn_prefill(q, k, v, o, lse=None, scale=None, causal=True, stream=None) -> None:
@@ -389,22 +354,12 @@ def kv_append_fp8(k_cache, v_cache, k_new, v_new, k_scale, v_scale, cache_lens, 
     _check("kv_append_fp8", st)
 
 
+# The calls from here on marshal their arguments in _marshal (binding/marshal.cpp).
 # ------------------------------------------- sliding window with first tokens visible
 def attn_prefill_window(q, k, v, o, window, sinks=0, lse=None, scale=None, stream=None) -> None:
     """``attn_prefill`` (causal) where the query at position p sees keys j <= p with
     j > p - window or j < sinks."""
-    B, N, Hq, d = q.shape
-    Hkv = k.shape[2]
-    if k.shape != (B, N, Hkv, d) or v.shape != k.shape or o.shape != q.shape:
-        raise ValueError("shape mismatch")
-    if lse is not None and lse.shape != (B, Hq, N):
-        raise ValueError("lse must be [B, Hq, N]")
-    dev = _current(q, "q")
-    bf16 = torch.bfloat16
-    st = lib.attn_prefill_window(_at(q, "q", bf16, dev), _at(k, "k", bf16, dev), _at(v, "v", bf16, dev),
-                                 _at(o, "o", None, dev), _out_dtype(o), _at(lse, "lse", torch.float32, dev),
-                                 B, Hq, Hkv, N, d, d ** -0.5 if scale is None else scale, _int32(window),
-                                 _int32(sinks), _stream(stream))
+    st = _marshal.prefill_window(*_here(q, stream), q, k, v, o, window, sinks, lse, scale)
     _check("attn_prefill_window", st)
 
 
@@ -412,19 +367,8 @@ def attn_prefill_cache_window(q, k_cache, v_cache, seqlens_k, o, window, sinks=0
                               scale=None, stream=None) -> None:
     """``attn_prefill_cache`` (causal) with the mask of ``attn_prefill_window``; positions count
     from the start of the cached sequence."""
-    B, Nq, Hq, d = q.shape
-    max_blocks, num_blocks, cap, Hkv = _cache_fits(k_cache, v_cache, page_table, seqlens_k, B, d)
-    if o.shape != q.shape:
-        raise ValueError("shape mismatch")
-    if lse is not None and lse.shape != (B, Hq, Nq):
-        raise ValueError("lse must be [B, Hq, Nq]")
-    dev = _current(q, "q")
-    bf16, i32 = torch.bfloat16, torch.int32
-    st = lib.attn_prefill_cache_window(
-        _at(q, "q", bf16, dev), _at(k_cache, "k_cache", bf16, dev), _at(v_cache, "v_cache", bf16, dev),
-        _at(seqlens_k, "seqlens_k", i32, dev), _at(page_table, "page_table", i32, dev), max_blocks, num_blocks, cap,
-        _at(o, "o", None, dev), _out_dtype(o), _at(lse, "lse", torch.float32, dev), B, Nq, Hq, Hkv, d,
-        d ** -0.5 if scale is None else scale, _int32(window), _int32(sinks), _stream(stream))
+    st = _marshal.prefill_cache_window(*_here(q, stream), q, k_cache, v_cache, seqlens_k, o, window, sinks, lse,
+                                       page_table, scale)
     _check("attn_prefill_cache_window", st)
 
 
@@ -442,42 +386,37 @@ def decode_window_workspace(B, T, Hq, Hkv, d, max_seqlen_k, window, sinks=0, num
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _decode_window(fn, name, q, k_cache, v_cache, scales, seqlens_k, o, window, sinks, lse, page_table, max_seqlen_k,
-                   scale, num_splits, workspace, stream) -> None:
-    B, T, Hq, d = q.shape
-    max_blocks, num_blocks, cap, Hkv = _cache_fits(k_cache, v_cache, page_table, seqlens_k, B, d)
-    if o.shape != q.shape:
-        raise ValueError("shape mismatch")
-    if lse is not None and lse.shape != (B, Hq, T):
-        raise ValueError("lse must be [B, Hq, T]")
-    dev = _current(q, "q")
-    if workspace is None:
-        msk = max_seqlen_k if max_seqlen_k else (cap if page_table is None else max_blocks * 16)
-        workspace = decode_window_workspace(B, T, Hq, Hkv, d, msk, window, sinks, num_splits, q.device)
-    caches, more = _caches(k_cache, v_cache, scales, Hkv, dev)
-    i32 = torch.int32
-    st = fn(_at(q, "q", torch.bfloat16, dev), *caches, *more, _at(seqlens_k, "seqlens_k", i32, dev),
-            _at(page_table, "page_table", i32, dev), max_blocks, num_blocks, cap, max_seqlen_k,
-            _at(o, "o", None, dev), _out_dtype(o), _at(lse, "lse", torch.float32, dev), B, T, Hq, Hkv, d,
-            d ** -0.5 if scale is None else scale, _int32(window), _int32(sinks), num_splits,
-            _at(workspace, "workspace", None, dev), workspace.nbytes, _stream(stream))
-    _check(name, st)
+def _longest(k_cache, page_table, max_seqlen_k) -> int:
+    """The bound on the lengths: max_seqlen_k, or the cache's capacity where that is 0."""
+    return max_seqlen_k or int(k_cache.shape[1] if page_table is None else page_table.shape[1] * 16)
 
 
 def attn_decode_window(q, k_cache, v_cache, seqlens_k, o, window, sinks=0, lse=None, page_table=None, max_seqlen_k=0,
                        scale=None, num_splits=0, workspace=None, stream=None) -> None:
     """``attn_decode`` (causal) where token t, at position p = seqlens_k[b] - T + t, sees keys
     j <= p with j > p - window or j < sinks.  Only the blocks holding such keys are read."""
-    _decode_window(lib.attn_decode_window, "attn_decode_window", q, k_cache, v_cache, None, seqlens_k, o, window,
-                   sinks, lse, page_table, max_seqlen_k, scale, num_splits, workspace, stream)
+    here = _here(q, stream)
+    if workspace is None:
+        workspace = decode_window_workspace(*q.shape[:3], k_cache.shape[2], q.shape[3],
+                                            _longest(k_cache, page_table, max_seqlen_k), window, sinks, num_splits,
+                                            q.device)
+    st = _marshal.decode_window(*here, q, k_cache, v_cache, None, None, seqlens_k, o, window, sinks, lse, page_table,
+                                max_seqlen_k, scale, num_splits, workspace)
+    _check("attn_decode_window", st)
 
 
 def attn_decode_window_fp8(q, k_cache, v_cache, k_scale, v_scale, seqlens_k, o, window, sinks=0, lse=None,
                            page_table=None, max_seqlen_k=0, scale=None, num_splits=0, workspace=None,
                            stream=None) -> None:
     """``attn_decode_window`` over an FP8 cache (arguments as ``attn_decode_fp8``)."""
-    _decode_window(lib.attn_decode_window_fp8, "attn_decode_window_fp8", q, k_cache, v_cache, (k_scale, v_scale),
-                   seqlens_k, o, window, sinks, lse, page_table, max_seqlen_k, scale, num_splits, workspace, stream)
+    here = _here(q, stream)
+    if workspace is None:
+        workspace = decode_window_workspace(*q.shape[:3], k_cache.shape[2], q.shape[3],
+                                            _longest(k_cache, page_table, max_seqlen_k), window, sinks, num_splits,
+                                            q.device)
+    st = _marshal.decode_window(*here, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, o, window, sinks, lse,
+                                page_table, max_seqlen_k, scale, num_splits, workspace)
+    _check("attn_decode_window_fp8", st)
 
 
 # ------------------------------------------------------------------ shared prefix
@@ -494,31 +433,17 @@ def decode_shared_workspace(B, T, Hq, Hkv, d, max_seqlen_k, prefix_blocks, num_s
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _decode_shared(fn, name, q, k_cache, v_cache, scales, seqlens_k, page_table, prefix_table, o, lse, max_seqlen_k,
-                   scale, causal, num_splits, workspace, stream) -> None:
-    B, T, Hq, d = q.shape
-    if page_table is None:
-        raise ValueError("a shared prefix needs a page table")
-    max_blocks, num_blocks, _, Hkv = _cache_fits(k_cache, v_cache, page_table, seqlens_k, B, d)
-    if o.shape != q.shape:
-        raise ValueError("shape mismatch")
-    if prefix_table.dim() != 1:
-        raise ValueError("prefix_table must be [prefix_blocks]")
-    if lse is not None and lse.shape != (B, Hq, T):
-        raise ValueError("lse must be [B, Hq, T]")
-    n = prefix_table.shape[0]
-    dev = _current(q, "q")
+def _decode_shared(name, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_table, prefix_table, o, lse,
+                   max_seqlen_k, scale, causal, num_splits, workspace, stream) -> None:
+    here = _here(q, stream)
     if workspace is None:
-        msk = max_seqlen_k if max_seqlen_k else max_blocks * 16
-        workspace = decode_shared_workspace(B, T, Hq, Hkv, d, msk, n, num_splits, q.device)
-    caches, more = _caches(k_cache, v_cache, scales, Hkv, dev)
-    i32 = torch.int32
-    st = fn(_at(q, "q", torch.bfloat16, dev), *caches, *more, _at(seqlens_k, "seqlens_k", i32, dev),
-            _at(page_table, "page_table", i32, dev), max_blocks, num_blocks,
-            _at(prefix_table, "prefix_table", i32, dev) if n else None, n, max_seqlen_k, _at(o, "o", None, dev),
-            _out_dtype(o), _at(lse, "lse", torch.float32, dev), B, T, Hq, Hkv, d,
-            d ** -0.5 if scale is None else scale, bool(causal), num_splits,
-            _at(workspace, "workspace", None, dev), workspace.nbytes, _stream(stream))
+        if page_table is None:
+            raise ValueError("a shared prefix needs a page table")
+        workspace = decode_shared_workspace(*q.shape[:3], k_cache.shape[2], q.shape[3],
+                                            _longest(k_cache, page_table, max_seqlen_k), prefix_table.shape[0],
+                                            num_splits, q.device)
+    st = _marshal.decode_shared(*here, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_table, prefix_table, o,
+                                lse, max_seqlen_k, scale, causal, num_splits, workspace)
     _check(name, st)
 
 
@@ -528,17 +453,16 @@ def attn_decode_shared(q, k_cache, v_cache, seqlens_k, page_table, prefix_table,
     first blocks: prefix_table int32 ``[prefix_blocks]`` names them (``page_table[0, :n]`` serves)
     and page_table's first prefix_blocks columns are not read.  The prefix is read once for the
     whole batch.  seqlens_k counts the prefix and the T new tokens."""
-    _decode_shared(lib.attn_decode_shared, "attn_decode_shared", q, k_cache, v_cache, None, seqlens_k, page_table,
-                   prefix_table, o, lse, max_seqlen_k, scale, causal, num_splits, workspace, stream)
+    _decode_shared("attn_decode_shared", q, k_cache, v_cache, None, None, seqlens_k, page_table, prefix_table, o, lse,
+                   max_seqlen_k, scale, causal, num_splits, workspace, stream)
 
 
 def attn_decode_shared_fp8(q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_table, prefix_table, o, lse=None,
                            max_seqlen_k=0, scale=None, causal=True, num_splits=0, workspace=None,
                            stream=None) -> None:
     """``attn_decode_shared`` over an FP8 cache (scales as ``attn_decode_fp8``)."""
-    _decode_shared(lib.attn_decode_shared_fp8, "attn_decode_shared_fp8", q, k_cache, v_cache, (k_scale, v_scale),
-                   seqlens_k, page_table, prefix_table, o, lse, max_seqlen_k, scale, causal, num_splits, workspace,
-                   stream)
+    _decode_shared("attn_decode_shared_fp8", q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_table,
+                   prefix_table, o, lse, max_seqlen_k, scale, causal, num_splits, workspace, stream)
 
 
 # ------------------------------------------------- norm, rotation and append in one pass
@@ -547,9 +471,9 @@ def rope_table_fill(table, theta=10000.0, stream=None) -> None:
     then the sines (angles in 64 bits)."""
     if table.dim() != 2:
         raise ValueError("table must be [rows, rot_dim]")
-    dev = _current(table, "table")
-    _check("rope_table_fill", lib.rope_table_fill(_at(table, "table", torch.float32, dev), int(table.shape[0]),
-                                                  int(table.shape[1]), float(theta), _stream(stream)))
+    _, handle = _here(table, stream)
+    _check("rope_table_fill", lib.rope_table_fill(_dev(table, "table", torch.float32), int(table.shape[0]),
+                                                  int(table.shape[1]), float(theta), handle))
 
 
 def rope_table(rows, rot_dim, theta=10000.0, device="cuda", stream=None) -> torch.Tensor:
@@ -559,88 +483,32 @@ def rope_table(rows, rot_dim, theta=10000.0, device="cuda", stream=None) -> torc
     return table
 
 
-def _token_rows(t, name, dev):
-    """Pointer and token stride (elements) of a bf16 ``[B, T, H, d]`` tensor whose tokens' rows are
-    contiguous and evenly spaced over B * T: contiguous, or a view of a fused projection output."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, like the other tensors")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}")
-    B, T, H, d = t.shape
-    sb, st, sh, sd = t.stride()
-    step = st if T > 1 else (sb if B > 1 else H * d)
-    if (d > 1 and sd != 1) or (H > 1 and sh != d) or (B > 1 and T > 1 and sb != T * st):
-        raise ValueError(f"{name}: each token's heads must be contiguous and the tokens evenly spaced")
-    return t.data_ptr(), step
-
-
-def _norm_rope_args(q_weight, k_weight, rope, d, dev):
-    """q_weight, k_weight and the angle table with its sizes, as the C calls take them."""
-    for w in (q_weight, k_weight):
-        if w is not None and w.shape != (d,):
-            raise ValueError("q_weight and k_weight must be [d]")
-    qw, kw = _at(q_weight, "q_weight", torch.bfloat16, dev), _at(k_weight, "k_weight", torch.bfloat16, dev)
-    if rope is None:
-        return qw, kw, None, 0, 0
-    rows, rot = rope.shape
-    return qw, kw, _at(rope, "rope", torch.float32, dev), rows, rot
-
-
 def qk_norm_rope(q, k, q_out, k_out, rope, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, pos0=None,
                  stream=None) -> None:
     """Per-head RMS norm (with a weight ``[d]``) and rotation of q ``[B, T, Hq, d]`` and k
     ``[B, T, Hkv, d]`` bf16, which may be views of a fused projection output, into contiguous q_out
     and k_out.  rope fp32 ``[rows, rot_dim]`` (``rope_table``) or None; pos0 int32 ``[B]`` is the
     position of each sequence's token 0 (default 0)."""
-    B, T, Hq, d = q.shape
-    Hkv = k.shape[2]
-    if k.shape != (B, T, Hkv, d) or q_out.shape != q.shape or k_out.shape != k.shape:
-        raise ValueError("shape mismatch")
-    if pos0 is not None and pos0.shape != (B,):
-        raise ValueError("pos0 must be [B]")
-    dev = _current(q, "q")
-    qp, qs = _token_rows(q, "q", dev)
-    kp, ks = _token_rows(k, "k", dev)
-    qw, kw, tab, rows, rot = _norm_rope_args(q_weight, k_weight, rope, d, dev)
-    st = lib.qk_norm_rope(qp, kp, qs, ks, _at(q_out, "q_out", torch.bfloat16, dev),
-                          _at(k_out, "k_out", torch.bfloat16, dev), qw, kw, eps, tab, rows, rot, bool(interleaved),
-                          _at(pos0, "pos0", torch.int32, dev), B, T, Hq, Hkv, d, _stream(stream))
+    st = _marshal.norm_rope(*_here(q, stream), q, k, q_out, k_out, rope, q_weight, k_weight, eps, interleaved, pos0)
     _check("qk_norm_rope", st)
-
-
-def _append_norm_rope(fn, name, k_cache, v_cache, q, k_new, v_new, q_out, scales, rope, cache_lens, page_table,
-                      q_weight, k_weight, eps, interleaved, stream) -> None:
-    B, T, Hq, d = q.shape
-    max_blocks, num_blocks, cap, Hkv = _cache_fits(k_cache, v_cache, page_table, cache_lens, B, d)
-    if k_new.shape != (B, T, Hkv, d) or v_new.shape != k_new.shape or q_out.shape != q.shape:
-        raise ValueError("shape mismatch")
-    dev = _current(q, "q")
-    qp, qs = _token_rows(q, "q", dev)
-    kp, ks = _token_rows(k_new, "k_new", dev)
-    vp, vs = _token_rows(v_new, "v_new", dev)
-    caches, more = _caches(k_cache, v_cache, scales, Hkv, dev)
-    qw, kw, tab, rows, rot = _norm_rope_args(q_weight, k_weight, rope, d, dev)
-    st = fn(*caches, qp, kp, vp, qs, ks, vs, _at(q_out, "q_out", torch.bfloat16, dev), *more, qw, kw, eps, tab, rows,
-            rot, bool(interleaved), _at(cache_lens, "cache_lens", torch.int32, dev),
-            _at(page_table, "page_table", torch.int32, dev), max_blocks, num_blocks, cap, B, T, Hq, Hkv, d,
-            _stream(stream))
-    _check(name, st)
 
 
 def kv_append_norm_rope(k_cache, v_cache, q, k_new, v_new, q_out, rope, cache_lens, page_table=None, q_weight=None,
                         k_weight=None, eps=1e-6, interleaved=False, stream=None) -> None:
     """``qk_norm_rope`` of the new tokens at positions cache_lens[b] + t, with the keys and values
     written to the cache (as ``kv_append``) and the queries to q_out ``[B, T, Hq, d]``."""
-    _append_norm_rope(lib.kv_append_norm_rope, "kv_append_norm_rope", k_cache, v_cache, q, k_new, v_new, q_out, None,
-                      rope, cache_lens, page_table, q_weight, k_weight, eps, interleaved, stream)
+    st = _marshal.append_norm_rope(*_here(q, stream), k_cache, v_cache, q, k_new, v_new, q_out, None, None, rope,
+                                   cache_lens, page_table, q_weight, k_weight, eps, interleaved)
+    _check("kv_append_norm_rope", st)
 
 
 def kv_append_norm_rope_fp8(k_cache, v_cache, q, k_new, v_new, q_out, k_scale, v_scale, rope, cache_lens,
                             page_table=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
                             stream=None) -> None:
     """``kv_append_norm_rope`` into an FP8 cache (quantised as ``kv_append_fp8`` does)."""
-    _append_norm_rope(lib.kv_append_norm_rope_fp8, "kv_append_norm_rope_fp8", k_cache, v_cache, q, k_new, v_new, q_out,
-                      (k_scale, v_scale), rope, cache_lens, page_table, q_weight, k_weight, eps, interleaved, stream)
+    st = _marshal.append_norm_rope(*_here(q, stream), k_cache, v_cache, q, k_new, v_new, q_out, k_scale, v_scale,
+                                   rope, cache_lens, page_table, q_weight, k_weight, eps, interleaved)
+    _check("kv_append_norm_rope_fp8", st)
 
 
 def kv_cache_bytes(n_layers, batch, tokens, n_kv_heads, head_dim, elem_bytes) -> int:

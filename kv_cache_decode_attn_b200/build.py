@@ -1,10 +1,12 @@
-"""Build ``libkvattn.so`` in-tree with nvcc for sm_100a.
+"""Build ``libkvattn.so`` in-tree with nvcc for sm_100a, and the binding's ``_marshal.so``.
 
 ``python kv_cache_decode_attn_b200/build.py`` (or ``build()``) compiles every
 ``csrc/*.cu`` and ``csrc/*.cpp`` file into one shared library beside this file.  The library links
 the CUDA runtime statically and reaches the driver API (tensor-map encoding)
 through ``cudaGetDriverEntryPointByVersion``, so it needs no ``-lcuda`` at link
-time.  Rebuilds only when a source is newer than the library.
+time.  ``binding/marshal.cpp`` (argument checks of the Python binding, compiled against
+the installed torch's headers) becomes ``_marshal.so``, which calls the library beside it.
+Rebuilds only when a source is newer than what it makes.
 """
 
 from __future__ import annotations
@@ -19,6 +21,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libkvattn.so")
+BINDING = os.path.join(HERE, "binding", "marshal.cpp")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -46,8 +50,33 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    header = os.path.join(INCLUDE, "attn.h")
+    if not force and os.path.exists(MARSHAL) and \
+            os.path.getmtime(MARSHAL) > max(os.path.getmtime(BINDING), os.path.getmtime(header)):
+        return MARSHAL
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    inc = [f"-I{INCLUDE}", f"-isystem{sysconfig.get_paths()['include']}"]
+    inc += [f"-isystem{d}" for d in cpp_extension.include_paths()]
+    tmp = MARSHAL + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, BINDING, "-o", tmp,
+           f"-L{HERE}", "-l:libkvattn.so", "-Wl,-rpath,$ORIGIN",
+           *(f"-L{d}" for d in cpp_extension.library_paths()), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
+        build_binding(force, verbose)
         return LIB
     nvcc = _nvcc()
     objs = []
@@ -65,6 +94,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     cmd = [nvcc, *ARCH_FLAGS, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    build_binding(force, verbose)
     return LIB
 
 
