@@ -91,12 +91,14 @@ struct DecodeLayout {
   int R, chunk, max_chunks;
   int balanced, n_chunks;   // balanced split: chunks over the batch (per KV head)
   int stream;               // CTAs per KV head with even shares of its tiles
+  int direct;               // one chunk per sequence, no combine
   size_t o_bytes, lse_offset, plan_offset, total;
 };
 
-// sel: the windowed and shared-prefix calls' splitting, max_seqlen_k being the longest selected range
+// sel: the windowed and shared-prefix calls' splitting, max_seqlen_k being the longest selected range;
+// whole: outputs may come from one CTA per (sequence, KV head)
 bool decode_layout(int B, int T, int Hq, int Hkv, int d, int max_seqlen_k, int num_splits, bool fp8,
-                   DecodeLayout* out, bool sel = false) {
+                   DecodeLayout* out, bool sel = false, bool whole = false) {
   if (B < 1 || T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || max_seqlen_k < 1 || num_splits < 0) return false;
   if (max_seqlen_k > kMaxDecodeSeqlen) return false;
   if (d != 64 && d != 128) return false;
@@ -108,7 +110,15 @@ bool decode_layout(int B, int T, int Hq, int Hkv, int d, int max_seqlen_k, int n
   L.n_chunks = 0;
   size_t items = (size_t)B * Hkv * L.max_chunks;
   L.stream = 0;
-  if (sel && num_splits == 0 && !decode_uses_tc(L.R, fp8)) {
+  const bool tc = decode_uses_tc(L.R, fp8);
+  L.direct = whole && num_splits == 0 &&
+             decode_direct((long long)B * Hkv * (tc ? decode_row_tiles(T, Hq / Hkv) : 1), max_seqlen_k, tc);
+  if (L.direct) {
+    L.chunk = (max_seqlen_k + kDecodeTile - 1) / kDecodeTile * kDecodeTile;
+    L.max_chunks = 1;
+    L.balanced = 0;
+    items = (size_t)B * Hkv;
+  } else if (sel && num_splits == 0 && !tc) {
     L.stream = decode_stream_ctas(B, L.R, Hkv, max_seqlen_k, fp8);
     if (L.stream) items = ((size_t)L.stream + B) * Hkv;
   }
@@ -260,7 +270,7 @@ int decode_impl(const void* q, const void* k_cache, const void* v_cache, const f
   if (window >= max_seqlen_k || sinks >= max_seqlen_k) window = 0;   // every key up to the own one: plain decode
   const int max_keys = window > 0 ? window_max_keys(max_seqlen_k, T, window, sinks) : max_seqlen_k;
   DecodeLayout L;
-  if (!decode_layout(B, T, Hq, Hkv, d, max_keys, num_splits, fp8, &L, window > 0)) return ATTN_ERR_INVALID_ARG;
+  if (!decode_layout(B, T, Hq, Hkv, d, max_keys, num_splits, fp8, &L, window > 0, window > 0)) return ATTN_ERR_INVALID_ARG;
   if (workspace_bytes < L.total) return ATTN_ERR_WORKSPACE;
   if (static_scratch) {
     // attn_decode_noalloc: the library's own array, looked up only once the request is known to be valid
@@ -335,6 +345,7 @@ int decode_impl(const void* q, const void* k_cache, const void* v_cache, const f
     a.sel.window = window;
     a.sel.sinks = sinks;
     a.stream = L.stream;
+    a.direct = L.direct;
   }
   return cuda_status(launch_decode(a, static_cast<cudaStream_t>(stream)), name);
 }
@@ -720,8 +731,8 @@ size_t attn_decode_window_workspace_bytes(int B, int T, int Hq, int Hkv, int d, 
     return attn_decode_workspace_bytes(B, T, Hq, Hkv, d, max_seqlen_k, num_splits);
   const int max_keys = window_max_keys(max_seqlen_k, T, window, sinks);
   DecodeLayout L, L8;   // enough for either cache type, as attn_decode_workspace_bytes
-  if (!decode_layout(B, T, Hq, Hkv, d, max_keys, num_splits, false, &L, true)) return 0;
-  if (!decode_layout(B, T, Hq, Hkv, d, max_keys, num_splits, true, &L8, true)) return 0;
+  if (!decode_layout(B, T, Hq, Hkv, d, max_keys, num_splits, false, &L, true, true)) return 0;
+  if (!decode_layout(B, T, Hq, Hkv, d, max_keys, num_splits, true, &L8, true, true)) return 0;
   return std::max(L.total, L8.total);
 }
 

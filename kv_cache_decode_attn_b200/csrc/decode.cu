@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
     sk = seq_keys<SEL>(p.sel, p.seqlens, b, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
     if (sk.bad) {
       if (threadIdx.x == 0 && c == 0 && g == 0) atomicOr(p.status, DEV_SEQLEN);
-      return;   // the combine kernel writes NaN rows for this sequence
+      if (SEL && p.out.on) p.out.store_nan<D>(b, g, 0, p.R, threadIdx.x, blockDim.x);
+      return;   // else the combine kernel writes NaN rows for this sequence
     }
     tok_begin = c * p.chunk;
     if (tok_begin >= sk.L) return;
@@ -149,6 +150,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
   if constexpr (FP8) {
     if (!(SEL && p.stream) && bad_scale(g)) {
       if (threadIdx.x == 0 && c == 0) atomicOr(p.status, DEV_SCALE);
+      if (SEL && p.out.on) {
+        p.out.store_nan<D>(b, g, 0, p.R, threadIdx.x, blockDim.x);
+        return;
+      }
       for (int r = threadIdx.x; r < p.R; r += blockDim.x) p.part_lse[item * p.R + r] = NAN;
       return;   // the whole CTA leaves before any barrier: the scales are uniform across it
     }
@@ -451,6 +456,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
     constexpr int kC = C::kConsumerWarps * 32;
     if (consumers_abort<kC>(abort_flag)) {
       // a wait gave up: this segment and the rest of the share are left as NaN
+      if (p.out.on) {
+        p.out.store_nan<D>(b, g, 0, p.R, threadIdx.x, kC);
+        return;
+      }
       for (;;) {
         for (int r = threadIdx.x; r < p.R; r += kC) p.part_lse[item * p.R + r] = NAN;
         if (!p.stream || (x += n_tiles) >= x1) return;
@@ -536,10 +545,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
           }
         }
         const float inv = lsum > 0.f ? (FP8 ? v_scale / lsum : 1.f / lsum) : 0.f;
-        *reinterpret_cast<float4*>(p.part_o + (item * p.R + r) * (size_t)D + 4 * v) =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (v == 0)
-          p.part_lse[item * p.R + r] = bad ? NAN : (lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY);
+        const float4 out = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        const float lse = bad ? NAN : (lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY);
+        if (p.out.on) {
+          p.out.store4<D>(b, g, r, 4 * v, out);
+          if (v == 0) p.out.store_lse(b, g, r, lse);
+          continue;
+        }
+        *reinterpret_cast<float4*>(p.part_o + (item * p.R + r) * (size_t)D + 4 * v) = out;
+        if (v == 0) p.part_lse[item * p.R + r] = lse;
       }
     }
     if (!more) break;
@@ -905,6 +919,7 @@ SplitParams split_params(const DecodeLaunch& a) {
   sp.balanced = a.balanced;
   sp.plan = a.plan;
   sp.sel = a.sel;
+  if (a.direct) sp.out = direct_out(a);
   sp.B = a.B;
   sp.stream = a.stream;
   sp.early = a.early;
@@ -970,6 +985,17 @@ int decode_balanced_chunks(int B, int Hkv, int items_per_slot) {
   return n > B ? n : B;
 }
 
+bool decode_direct(long long units, int max_keys, bool tc) {
+  // Times in us, measured on B200: a 64-token tile of a CTA that has its SM to itself (bf16, the
+  // heads' rows of a 64-token tile wait for memory, the tensor-core kernel for its own chain of
+  // products); with more CTAs than SMs the tiles of two share the SM's bandwidth; and the partials
+  // and the combine of a split.  16 x 8 pairs with a window of 1024: 14.5 us a call against 19.7
+  // split; 1 x 8 pairs: 11.6 against 8.7.
+  const double tiles = (max_keys + kDecodeTile - 1) / kDecodeTile, sms = device_sms(), tile = tc ? 1.3 : 0.65;
+  const double waves = units <= sms ? 1.0 : 1.7 * ceil(units / (2 * sms));
+  return tiles * tile * waves <= tiles * 0.55 * units / sms + 5.0;
+}
+
 int decode_stream_ctas(int B, int R, int Hkv, int max_keys, bool fp8) {
   if (B > kStreamMaxB || (long long)B * ((max_keys + kDecodeTile - 1) / kDecodeTile) > INT32_MAX) return 0;
   const int per_sm = fp8 ? (R <= 8 ? 3 : (R <= 16 ? 2 : 1)) : 2;   // resident CTAs of the kernel
@@ -1022,7 +1048,7 @@ cudaError_t launch_decode_split(const DecodeLaunch& a, cudaStream_t stream) {
 
 cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream) {
   const cudaError_t e = launch_decode_split(a, stream);
-  return e != cudaSuccess ? e : launch_decode_combine(a, stream);
+  return e != cudaSuccess || a.direct ? e : launch_decode_combine(a, stream);
 }
 
 cudaError_t launch_decode_combine(const DecodeLaunch& a, cudaStream_t stream) {

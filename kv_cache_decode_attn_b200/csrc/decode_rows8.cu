@@ -119,7 +119,8 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
     sg.sk = seq_keys<true>(p.sel, p.seqlens, sg.b, p.T, p.max_seqlen, PAGED, p.capacity, p.max_blocks);
     if (sg.sk.bad) {
       if (threadIdx.x == 0 && c == 0 && sg.g == 0) atomicOr(p.status, DEV_SEQLEN);
-      return;   // the combine kernel writes NaN rows for this sequence
+      if (p.out.on) p.out.store_nan<D>(sg.b, sg.g, 0, p.R, threadIdx.x, blockDim.x);
+      return;   // else the combine kernel writes NaN rows for this sequence
     }
     sg.tok_begin = c * p.chunk;
     if (sg.tok_begin >= sg.sk.L) return;
@@ -349,6 +350,10 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
     // ------------------------------------------------ merge the four warps (the ring goes on)
     if (consumers_abort<kC>(abort_flag)) {
       // a wait gave up: this segment and the rest of the share are left as NaN
+      if (p.out.on) {
+        p.out.store_nan<D>(sg.b, sg.g, 0, p.R, threadIdx.x, kC);
+        return;
+      }
       for (;;) {
         for (int r = threadIdx.x; r < p.R; r += kC) p.part_lse[sg.item * p.R + r] = NAN;
         if (!p.stream || (x += sg.n_tiles) >= x1) return;
@@ -433,9 +438,15 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
           acc.w += y.w;
         }
         const float inv = lsum > 0.f ? (FP8 ? v_scale / lsum : 1.f / lsum) : 0.f;
-        *reinterpret_cast<float4*>(p.part_o + (item * p.R + r) * (size_t)D + 4 * v) =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (v == 0) p.part_lse[item * p.R + r] = bad ? NAN : (lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY);
+        const float4 out = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        const float lse = bad ? NAN : (lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY);
+        if (p.out.on) {   // sg is still this segment
+          p.out.store4<D>(sg.b, sg.g, r, 4 * v, bad ? make_float4(NAN, NAN, NAN, NAN) : out);
+          if (v == 0) p.out.store_lse(sg.b, sg.g, r, lse);
+          continue;
+        }
+        *reinterpret_cast<float4*>(p.part_o + (item * p.R + r) * (size_t)D + 4 * v) = out;
+        if (v == 0) p.part_lse[item * p.R + r] = lse;
       }
     }
     if (!more) break;

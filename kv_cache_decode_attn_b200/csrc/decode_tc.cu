@@ -132,6 +132,7 @@ struct TcParams {
   int* plan;                   // [B, 3] written by CTA 0 for the combine kernel
   KeySelect sel;               // SEL instances: which keys of a sequence the launch reads
   int early = 0, fence = 0;    // SEL instances: as in SplitParams
+  DirectOut out;
 };
 
 // Balanced split: the chunks of this launch and this CTA's (sequence, KV head, chunk),
@@ -314,6 +315,10 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
   // invalid lengths: their rows are made NaN by the combine kernel
   if (sk.bad) {
     if (SEL && threadIdx.x == 0) atomicOr(p.status, DEV_SEQLEN);
+    if (SEL && p.out.on) {
+      const int r0 = rt * p.TT * p.G;
+      p.out.store_nan<D>(b, g, r0, min(r0 + p.TT * p.G, p.R), threadIdx.x, blockDim.x);
+    }
     leave();
     return;
   }
@@ -354,7 +359,9 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
       // a scale that is not a positive finite number: the whole CTA leaves before any
       // barrier (the scales are uniform across it)
       if (threadIdx.x == 0 && c == 0 && rt == 0) atomicOr(p.status, DEV_SCALE);
-      for (int r = threadIdx.x; r < tile_rows; r += blockDim.x) p.part_lse[row0 + r] = NAN;
+      if (SEL && p.out.on) p.out.store_nan<D>(b, g, t0 * p.G, t0 * p.G + tile_rows, threadIdx.x, blockDim.x);
+      else
+        for (int r = threadIdx.x; r < tile_rows; r += blockDim.x) p.part_lse[row0 + r] = NAN;
       leave();
       return;
     }
@@ -770,7 +777,13 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
         uint32_t r[32];
         tmem_ld32(lane_base + C::kOCol + cc, r);
         tc_wait_ld();
-        if (live) {
+        if (SEL && live && p.out.on) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            p.out.store4<D>(b, g, t0 * p.G + row, cc + e,
+                            make_float4(__uint_as_float(r[e]) * inv_l, __uint_as_float(r[e + 1]) * inv_l,
+                                        __uint_as_float(r[e + 2]) * inv_l, __uint_as_float(r[e + 3]) * inv_l));
+        } else if (live) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<float4*>(out + cc + e) =
@@ -778,7 +791,11 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
                             __uint_as_float(r[e + 2]) * inv_l, __uint_as_float(r[e + 3]) * inv_l);
         }
       }
-      if (live) p.part_lse[row0 + row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      if (SEL && live && p.out.on) p.out.store_lse(b, g, t0 * p.G + row, lse);
+      else if (live) p.part_lse[row0 + row] = lse;
+    } else if (SEL && live && p.out.on) {
+      p.out.store_nan<D>(b, g, t0 * p.G + row, t0 * p.G + row + 1, 0, 1);
     } else if (live) {
       p.part_lse[row0 + row] = NAN;   // a wait gave up
     }
@@ -839,6 +856,7 @@ cudaError_t run_tc_as(const DecodeLaunch& a, const CUtensorMap& tk, const CUtens
   p.plan = a.plan;
   p.sel = a.sel;
   p.early = a.early;
+  if (a.direct) p.out = direct_out(a);
   p.fence = a.fence;
   if (a.balanced && (a.B > kBalancedMaxB || row_tiles != 1 || a.n_chunks < a.B)) return cudaErrorInvalidValue;
   auto kern = decode_tc_kernel<D, PAGED, FP8, SEL>;

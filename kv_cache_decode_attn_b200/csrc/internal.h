@@ -47,6 +47,11 @@ inline bool decode_balanced(int B, int T, int G, int num_splits, bool fp8) {
 // Chunks over the whole batch (per KV head) of the balanced split on the current device.
 int decode_balanced_chunks(int B, int Hkv, int items_per_slot = kBalancedItemsPerSlot);
 
+// Whether windowed decode (automatic splitting) gives each of its `units` -- (sequence, KV
+// head, row tile) -- to one CTA, which reads up to max_keys keys and writes the outputs
+// itself, rather than split them over the SMs and merge.  tc: the tensor-core kernel's.
+bool decode_direct(long long units, int max_keys, bool tc);
+
 // Windowed and shared-prefix decode (the SEL instances) on the warp-level kernels, automatic
 // splitting: this many CTAs per KV head share its tiles evenly (0: too many sequences or tiles for it,
 // one CTA per chunk then).
@@ -112,6 +117,7 @@ struct DecodeLaunch {
   const float* k_scale = nullptr;  // [Hkv]
   const float* v_scale = nullptr;
   KeySelect sel;
+  int direct = 0;   // sel, max_chunks == 1: the split kernel writes o and lse itself, no combine
   int stream = 0;   // sel, > 0: CTAs per KV head that share its tiles evenly; stream + B partials per KV head
   int early = 0;    // the split kernel lets the next one start at once (one with fence set)
   int fence = 0;    // the split kernel runs beside the one before, and ends after it

@@ -5,11 +5,57 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <math.h>
 
 #include "internal.h"
 #include "ptx.cuh"
 
 namespace kvattn {
+
+// SEL instances, one chunk per sequence (on): the split kernel writes the outputs itself.
+struct DirectOut {
+  int on = 0, o_bf16 = 0, T = 0, Hq = 0, G = 0;
+  void* o = nullptr;      // [B, T, Hq, D]
+  float* lse = nullptr;   // [B, Hq, T], or none
+
+  // columns col .. col + 3 of row r = t * G + head of the group, of sequence b and KV head g
+  template <int D>
+  __device__ __forceinline__ void store4(int b, int g, int r, int col, float4 v) const {
+    const int t = r / G, h = g * G + r - t * G;
+    const size_t at = (((size_t)b * T + t) * Hq + h) * D + col;
+    if (o_bf16) {
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o) + at) =
+          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    } else {
+      *reinterpret_cast<float4*>(static_cast<float*>(o) + at) = v;
+    }
+  }
+  __device__ __forceinline__ void store_lse(int b, int g, int r, float v) const {
+    const int t = r / G, h = g * G + r - t * G;
+    if (lse) lse[((size_t)b * Hq + h) * T + t] = v;
+  }
+  // rows r0 .. r1 - 1 as NaN, by threads `thread` of `threads`
+  template <int D>
+  __device__ __forceinline__ void store_nan(int b, int g, int r0, int r1, int thread, int threads) const {
+    for (int i = thread; i < (r1 - r0) * (D / 4); i += threads) {
+      const int r = r0 + i / (D / 4), col = i % (D / 4) * 4;
+      store4<D>(b, g, r, col, make_float4(NAN, NAN, NAN, NAN));
+      if (col == 0) store_lse(b, g, r, NAN);
+    }
+  }
+};
+
+inline DirectOut direct_out(const DecodeLaunch& a) {
+  DirectOut d;
+  d.on = 1;
+  d.o_bf16 = a.o_bf16;
+  d.T = a.T;
+  d.Hq = a.Hq;
+  d.G = a.Hq / a.Hkv;
+  d.o = a.o;
+  d.lse = a.lse;
+  return d;
+}
 
 struct SplitParams {
   const __nv_bfloat16* q;
@@ -27,6 +73,7 @@ struct SplitParams {
   int balanced = 0;            // tensor-core balanced split: partials indexed by the plan
   const int* plan = nullptr;   // [B, 3]: first chunk, chunks, chunk length per sequence
   KeySelect sel;               // SEL instances: which keys of a sequence the launch reads
+  DirectOut out;
   int B = 0;
   int stream = 0;              // SEL instances, > 0: CTAs per KV head that share its tiles evenly (see StreamPlan)
   int early = 0;               // SEL instances: let the next kernel start at once; it waits for this one
