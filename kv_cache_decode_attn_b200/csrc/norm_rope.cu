@@ -12,11 +12,13 @@
 // d / 16 threads share a row, 16 values each, chosen so that a thread holds both
 // members of each of its pairs: only the sum of squares crosses threads (2 or 3
 // shuffles).  A warp takes the same 4 (d = 128) or 8 heads of kTokens consecutive tokens,
-// the next token's values on their way while one is computed; the weights are unpacked
-// once, positions and addresses step from token to token, and values are computed in
-// pairs (f32x2).  Bound by HBM once that is so: with indexes divided out per row and single
-// fp32 operations the issue slots were 72 % busy and 4 x 4096 tokens of 32 + 8 + 8 heads
-// (405 MB) took 93 to 130 us.
+// all of whose loads go out first; meanwhile the CTA fetches the tokens' angle rows and
+// cache rows into shared memory, once for all heads; the weights are unpacked once, and
+// values are computed in pairs (f32x2).
+// 4 x 4096 tokens of 32 + 8 + 8 heads (405 MB; 62 us at the copy rate): 93 us with one
+// token per warp, indexes divided out per row and single fp32 operations (issue slots
+// 72 % busy); 98 with the angles read per token by each warp (waiting for them);
+// 80 as it is, with three CTAs per SM (99 without that bound on the registers).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -58,7 +60,7 @@ __device__ __forceinline__ void unpack8(uint4 u, F2 (&x)[4]) {
 }
 
 __device__ __forceinline__ void load8f(const float* src, F2 (&x)[4]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(src)), b = __ldg(reinterpret_cast<const float4*>(src) + 1);
+  const float4 a = reinterpret_cast<const float4*>(src)[0], b = reinterpret_cast<const float4*>(src)[1];
   x[0] = f2(a.x, a.y);
   x[1] = f2(a.z, a.w);
   x[2] = f2(b.x, b.y);
@@ -88,9 +90,12 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* dst, const F2 (&x)[4], floa
 
 // head_blocks: CTAs per token group, each with blockDim / 32 groups of heads
 template <int D, int kTokens, bool CACHED, bool FP8>
-__global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeLaunch a, int head_blocks) {
+__global__ void __launch_bounds__(256, 3) norm_rope_kernel(const NormRopeLaunch a, int head_blocks) {
   constexpr int kLanes = D / 16;       // threads per row
   constexpr int kHeads = 32 / kLanes;  // rows (heads of one token) per warp
+  __shared__ __align__(16) float angles[kTokens][D];         // rot / 2 cosines, then rot / 2 sines
+  __shared__ long long cache_row[kTokens];     // CACHED: row of the token in the [rows, Hkv, D] view, or -1
+  __shared__ int in_table[kTokens];            // whether the position is in the angle table
   const int tg = blockIdx.x / head_blocks;
   const int lane = threadIdx.x & 31, j = lane & (kLanes - 1);
   const int row = ((blockIdx.x - tg * head_blocks) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kHeads + lane / kLanes;
@@ -98,9 +103,8 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeLaunch a, 
   const int h = live ? row : 0;
   const bool is_q = h < a.Hq, is_v = CACHED && h >= a.Hq + a.Hkv;
   const int g = is_q ? h : (is_v ? h - a.Hq - a.Hkv : h - a.Hq);   // head among its kind
-  int tok = tg * kTokens;
-  const int n_tok = min(kTokens, a.B * a.T - tok);
-  int b = tok / a.T, t = tok - b * a.T;
+  const int tok0 = tg * kTokens;
+  const int n_tok = min(kTokens, a.B * a.T - tok0);
 
   // this thread's two vectors of 8 values: both halves of its rotated pairs, or (past the
   // rotated part, or with adjacent pairs) two neighbouring vectors
@@ -109,10 +113,15 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeLaunch a, 
   const bool turns = !is_v && (a.interleaved ? 16 * j < a.rot : j < n_rot);   // rot is a multiple of 16
 
   const long long stride = is_q ? a.q_stride : (is_v ? a.v_stride : a.k_stride);
-  const __nv_bfloat16* src = (is_q ? a.q : (is_v ? a.v : a.k)) + tok * stride + g * D;
+  const __nv_bfloat16* src = (is_q ? a.q : (is_v ? a.v : a.k)) + tok0 * stride + g * D;
   grid_dependency_wait();              // launched while the kernel before ends
-  uint4 n0 = *reinterpret_cast<const uint4*>(src + 8 * v0), n1 = *reinterpret_cast<const uint4*>(src + 8 * v1);
-  int first = a.pos0 ? __ldg(a.pos0 + b) : 0;
+  uint4 u0[kTokens], u1[kTokens];
+#pragma unroll
+  for (int n = 0; n < kTokens; ++n) {
+    const __nv_bfloat16* at = src + min(n, n_tok - 1) * stride;
+    u0[n] = *reinterpret_cast<const uint4*>(at + 8 * v0);
+    u1[n] = *reinterpret_cast<const uint4*>(at + 8 * v1);
+  }
   const __nv_bfloat16* weight = is_q ? a.q_weight : (is_v ? nullptr : a.k_weight);
   F2 w0[4], w1[4];
   if (weight) {
@@ -127,39 +136,61 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeLaunch a, 
     scale_ok = ks > 0.f && ks <= 3.402823466e38f && vs > 0.f && vs <= 3.402823466e38f;
     scale = is_v ? vs : ks;
   }
+
+  // token n's row of the angle table, or -1 outside it; CACHED: its row of the [rows, Hkv, D]
+  // view of the cache, as kv_append places it, or -1 (outside the table, too: the cache keeps
+  // what it holds)
+  auto find = [&](int n, long long& angle_row, long long& dst) {
+    const int tok = tok0 + n, b = tok / a.T;
+    const long long pos = (a.pos0 ? (long long)__ldg(a.pos0 + b) : 0) + (tok - b * a.T);
+    angle_row = a.rot == 0 ? 0 : (pos >= 0 && pos < a.rope_rows ? pos : -1);
+    dst = -1;
+    if (!CACHED || angle_row < 0) return;
+    if (pos < 0 || pos >= (a.page_table ? (long long)a.max_blocks * kPageTokens : (long long)a.capacity)) {
+      atomicOr(a.status, DEV_APPEND_RANGE);
+    } else if (!a.page_table) {
+      dst = (long long)b * a.capacity + pos;
+    } else {
+      const int blk = __ldg(a.page_table + (long long)b * a.max_blocks + pos / kPageTokens);
+      if (blk >= 0 && blk < a.num_blocks) dst = (long long)blk * kPageTokens + pos % kPageTokens;
+      else atomicOr(a.status, DEV_PAGE_ID);
+    }
+  };
+  long long own_row = 0, own_dst = -1;   // kTokens == 1: each thread looks for itself
+  if constexpr (kTokens == 1) {
+    find(0, own_row, own_dst);
+    if (own_row < 0 && j == 0) atomicOr(a.status, DEV_POSITION);
+  } else {
+    constexpr int kSide = 8;             // threads per token
+    for (int i = threadIdx.x; i < n_tok * kSide; i += blockDim.x) {
+      const int n = i / kSide, part = i % kSide;
+      long long at, dst;
+      find(n, at, dst);
+      if (at >= 0)
+        for (int e = 4 * part; e < a.rot; e += 4 * kSide)
+          *reinterpret_cast<float4*>(&angles[n][e]) = __ldg(reinterpret_cast<const float4*>(a.rope + at * a.rot + e));
+      if (part == 0) {
+        in_table[n] = at >= 0;
+        if (at < 0) atomicOr(a.status, DEV_POSITION);
+        cache_row[n] = dst;
+      }
+    }
+    __syncthreads();
+  }
+
   // dense rows (q_out, k_out) step from token to token
   const bool dense = is_q || !CACHED;
   const int heads = is_q ? a.Hq : a.Hkv;
-  __nv_bfloat16* out = (is_q ? a.q_out : a.k_out) + ((long long)tok * heads + g) * D;
+  __nv_bfloat16* out = (is_q ? a.q_out : a.k_out) + ((long long)tok0 * heads + g) * D;
 
-#pragma unroll 1
-  for (int n = 0; n < n_tok; ++n) {
-    const uint4 u0 = n0, u1 = n1;
-    const int at = first;
-    const int bb = b, tt = t;
-    if (kTokens > 1) {                 // the next token
-      if (++t == a.T) {
-        t = 0;
-        ++b;
-      }
-      if (n + 1 < n_tok) {
-        src += stride;
-        n0 = *reinterpret_cast<const uint4*>(src + 8 * v0);
-        n1 = *reinterpret_cast<const uint4*>(src + 8 * v1);
-        if (t == 0 && a.pos0) first = __ldg(a.pos0 + b);
-      }
-    }
-    const long long pos = (long long)at + tt;
-    const bool pos_ok = a.rot == 0 || (pos >= 0 && pos < a.rope_rows);
-    F2 c[4], s[4];
-    if (turns && pos_ok) {
-      const float* tab = a.rope + pos * a.rot + 8 * j;
-      load8f(tab, c);
-      load8f(tab + a.rot / 2, s);
-    }
+#pragma unroll
+  for (int n = 0; n < kTokens; ++n) {
+    if (kTokens > 1 && n >= n_tok) break;
+    const bool pos_ok = kTokens == 1 ? own_row >= 0 : in_table[n] != 0;
+    const long long dst_row = kTokens == 1 ? own_dst : cache_row[n];
     F2 x0[4], x1[4];
-    unpack8(u0, x0);
-    unpack8(u1, x1);
+    unpack8(u0[n], x0);
+    unpack8(u1[n], x1);
     if (any_weight) {
       F2 sq = mul2(x0[0], x0[0]);
 #pragma unroll
@@ -180,6 +211,10 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeLaunch a, 
       }
     }
     if (turns && pos_ok) {
+      F2 c[4], s[4];
+      const float* angle = kTokens == 1 ? a.rope + own_row * a.rot : angles[n];
+      load8f(angle + 8 * j, c);
+      load8f(angle + a.rot / 2 + 8 * j, s);
       if (!a.interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -200,54 +235,33 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeLaunch a, 
         }
       }
     }
-    __nv_bfloat16* const dst_dense = out;
-    if (dense) out += heads * D;
     if (!live) continue;
-    if (!pos_ok) {
-      if (j == 0) atomicOr(a.status, DEV_POSITION);
-      if (!dense) continue;   // the cache keeps what it holds
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x0[i] = x1[i] = f2(NAN, NAN);
-    }
     if (dense) {
-      store8(dst_dense + 8 * v0, x0);
-      store8(dst_dense + 8 * v1, x1);
+      if (!pos_ok) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x0[i] = x1[i] = f2(NAN, NAN);
+      }
+      __nv_bfloat16* dst = out + (long long)n * heads * D;
+      store8(dst + 8 * v0, x0);
+      store8(dst + 8 * v1, x1);
       continue;
     }
-    // K or V: the token's row of the cache, as kv_append places it
-    long long dst_row;
-    if (!a.page_table) {
-      if (pos < 0 || pos >= a.capacity) {
-        if (j == 0) atomicOr(a.status, DEV_APPEND_RANGE);
-        continue;
-      }
-      dst_row = ((long long)bb * a.capacity + pos) * a.Hkv + g;
-    } else {
-      if (pos < 0 || pos >= (long long)a.max_blocks * kPageTokens) {
-        if (j == 0) atomicOr(a.status, DEV_APPEND_RANGE);
-        continue;
-      }
-      const int blk = __ldg(a.page_table + (long long)bb * a.max_blocks + pos / kPageTokens);
-      if (blk < 0 || blk >= a.num_blocks) {
-        if (j == 0) atomicOr(a.status, DEV_PAGE_ID);
-        continue;
-      }
-      dst_row = ((long long)blk * kPageTokens + pos % kPageTokens) * a.Hkv + g;
-    }
+    if (dst_row < 0) continue;
+    const long long at = (dst_row * a.Hkv + g) * D;
     void* cache = is_v ? a.v_cache : a.k_cache;
     if constexpr (FP8) {
       if (!scale_ok) {
         if (j == 0) atomicOr(a.status, DEV_SCALE);
         continue;
       }
-      uint8_t* dst = static_cast<uint8_t*>(cache) + dst_row * D;
+      uint8_t* dst = static_cast<uint8_t*>(cache) + at;
       store8_e4m3(dst + 8 * v0, x0, scale);
       store8_e4m3(dst + 8 * v1, x1, scale);
     } else {
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(cache) + dst_row * D;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(cache) + at;
       if (is_v) {   // as it came
-        *reinterpret_cast<uint4*>(dst + 8 * v0) = u0;
-        *reinterpret_cast<uint4*>(dst + 8 * v1) = u1;
+        *reinterpret_cast<uint4*>(dst + 8 * v0) = u0[n];
+        *reinterpret_cast<uint4*>(dst + 8 * v1) = u1[n];
       } else {
         store8(dst + 8 * v0, x0);
         store8(dst + 8 * v1, x1);
@@ -274,8 +288,10 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float* table, int rows,
 }  // namespace
 
 namespace {
-// warps of a launch at one token each from which four tokens per warp pay: four waves of them
-constexpr long long kManyWarps = 4LL * 148 * 32;
+// Warps of a launch at one token each from which two, and four, tokens per warp pay.  Measured
+// (us at 1, 2, 4 tokens per warp): 19200 warps 10.8, 9.6, 11.5; 38400 19.9, 17.3, 17.0; 196608
+// 110, 92, 80; 192 (a decode step) 3.5, 4.9.
+constexpr long long kTwoFrom = 9600, kFourFrom = 32000;
 
 template <int D, int kTokens, bool CACHED, bool FP8>
 cudaError_t run_norm_rope(const NormRopeLaunch& a, int head_groups, cudaStream_t stream) {
@@ -290,8 +306,10 @@ cudaError_t run_norm_rope(const NormRopeLaunch& a, int head_groups, cudaStream_t
 template <int D, bool CACHED, bool FP8>
 cudaError_t run_norm_rope(const NormRopeLaunch& a, cudaStream_t stream) {
   const int heads = 32 / (D / 16), groups = (a.Hq + a.Hkv * (CACHED ? 2 : 1) + heads - 1) / heads;
-  return (long long)a.B * a.T * groups >= kManyWarps ? run_norm_rope<D, 4, CACHED, FP8>(a, groups, stream)
-                                                     : run_norm_rope<D, 1, CACHED, FP8>(a, groups, stream);
+  const long long warps = (long long)a.B * a.T * groups;
+  if (warps >= kFourFrom) return run_norm_rope<D, 4, CACHED, FP8>(a, groups, stream);
+  return warps >= kTwoFrom ? run_norm_rope<D, 2, CACHED, FP8>(a, groups, stream)
+                           : run_norm_rope<D, 1, CACHED, FP8>(a, groups, stream);
 }
 
 template <int D>
