@@ -278,13 +278,19 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
       return;
     }
   }
-  // TMEM first of all: a second CTA of the SM starts only once this one has given up its
-  // right to allocate (measured: 4.4 us after the first when that followed the plan)
-  if (warp == 0) {
-    tmem_alloc(tmem_slot, C::kTmemCols);
-    tmem_relinquish();
-  }
+  auto take_tmem = [&] {
+    if (warp == 0) {
+      tmem_alloc(tmem_slot, C::kTmemCols);
+      tmem_relinquish();
+    }
+  };
+  // SEL: TMEM first of all.  A second CTA of the SM starts only once this one has given up
+  // its right to allocate: 4.4 us after the first when that followed the plan.  (Long plain
+  // launches are no faster for it, and the FP8 ones measured 4 % slower with an SM's two
+  // CTAs in step.)
+  if constexpr (SEL) take_tmem();
   auto leave = [&] {   // the whole CTA, which has nothing to do
+    if (!SEL) return;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -406,6 +412,7 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
     }
   }
   fence_proxy_async_smem();
+  if constexpr (!SEL) take_tmem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

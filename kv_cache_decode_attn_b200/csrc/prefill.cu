@@ -476,14 +476,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kvh = itm.h / p.G;
       // WIN: position of the first key of tile t
       auto tile_pos = [&](int t) -> int { return t * kBN + (WIN && t >= itm.s_tiles ? itm.gap : 0); };
-      // paged: whether this lane's 16-token block of tile t (lanes >= 8: none) holds keys some row
-      // may see, and the physical block
+      // WIN: whether this lane's 16-token block of tile t (lanes >= 8: none) holds keys some row may see
       auto needs = [&](int t) -> bool {
         const int vt = t * kBN + lane * kPageTokens;
-        return lane < kBlocks && vt < itm.L && (!WIN || vt < p.sinks || tile_pos(t) + lane * kPageTokens >= itm.w0);
+        return lane < kBlocks && vt < itm.L && (vt < p.sinks || tile_pos(t) + lane * kPageTokens >= itm.w0);
       };
+      // paged: this lane's physical block of tile t (lanes >= 8 and blocks past L: none)
       auto read_id = [&](int t) -> int {
-        return needs(t) ? __ldg(p.page_table + (size_t)itm.b * p.max_blocks + tile_pos(t) / kPageTokens + lane) : -1;
+        if constexpr (WIN)
+          return needs(t) ? __ldg(p.page_table + (size_t)itm.b * p.max_blocks + tile_pos(t) / kPageTokens + lane) : -1;
+        const int nb = min(kBlocks, (itm.L - t * kBN + kPageTokens - 1) / kPageTokens);
+        return lane < nb ? __ldg(p.page_table + (size_t)itm.b * p.max_blocks + t * kBlocks + lane) : -1;
       };
       int id = 0;
       if constexpr (KV == KV_PAGED) id = read_id(0);
@@ -504,8 +507,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           // one 16-row box per 64 columns of d and physical block holding keys of this tile below L
-          const bool need = needs(t);
-          const int nb = __popc(__ballot_sync(0xffffffffu, need));
+          int nb = min(kBlocks, (itm.L - t * kBN + kPageTokens - 1) / kPageTokens);
+          bool need = lane < nb;
+          if constexpr (WIN) {
+            need = needs(t);
+            nb = __popc(__ballot_sync(0xffffffffu, need));
+          }
           int blk = id;
           if (need && (blk < 0 || blk >= p.num_blocks)) {
             atomicOr(p.status, DEV_PAGE_ID);
@@ -676,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j + 1 < n_kv0) issue_s(0, ksn);
         }
         if (sees_b(j)) {
-          ok = WIN && j == 0 && cols < kBN ? pv_narrow(1, st, cols, it) : pv_tile(1, st, first_b, it);
+          ok = WIN && j == 0 && cols < kBN ? pv_narrow(1, st, cols, it) : pv_tile(1, st, WIN ? first_b : j == 0, it);
           if (!ok) break;
           first_b = false;
         }
