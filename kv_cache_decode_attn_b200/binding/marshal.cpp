@@ -89,6 +89,12 @@ bool truth(PyObject* o) {
 
 void* stream_of(PyObject* o) { return PyLong_AsVoidPtr(o); }
 
+// Other Python threads run while the C call launches (a launch may wait for queue space).
+struct NoGil {
+  PyThreadState* state = PyEval_SaveThread();
+  ~NoGil() { PyEval_RestoreThread(state); }
+};
+
 // q [B, T, Hq, d] and the output of its shape, lse [B, Hq, T] or none.
 struct Queries {
   int B, T, Hq, d, o_type;
@@ -203,9 +209,12 @@ int prefill_window(PyObject* const* a) {
   const at::Tensor &k = tensor(a[3], "k"), &v = tensor(a[4], "v");
   if (k.dim() != 4 || k.size(0) != q.B || k.size(1) != q.T || k.size(3) != q.d || v.sizes() != k.sizes())
     refuse("shape mismatch");
-  return attn_prefill_window(q.q, typed(a[3], "k", at::kBFloat16, dev), typed(a[4], "v", at::kBFloat16, dev), q.o,
-                             q.o_type, q.lse, q.B, q.Hq, dim(k.size(2)), q.T, q.d, scale_or_default(a[9], q.d),
-                             i32(a[6]), i32(a[7]), stream_of(a[1]));
+  const void *kp = typed(a[3], "k", at::kBFloat16, dev), *vp = typed(a[4], "v", at::kBFloat16, dev);
+  const int Hkv = dim(k.size(2)), window = i32(a[6]), sinks = i32(a[7]);
+  const float scale = scale_or_default(a[9], q.d);
+  void* stream = stream_of(a[1]);
+  const NoGil free;
+  return attn_prefill_window(q.q, kp, vp, q.o, q.o_type, q.lse, q.B, q.Hq, Hkv, q.T, q.d, scale, window, sinks, stream);
 }
 
 // (dev, stream, q, k_cache, v_cache, seqlens, o, window, sinks, lse, page_table, scale)
@@ -213,9 +222,12 @@ int prefill_cache_window(PyObject* const* a) {
   const int dev = i32(a[0]);
   const Queries q(a[2], a[6], a[9], dev);
   const Cache c(a[3], a[4], Py_None, Py_None, a[5], a[10], q.B, q.d, dev);
+  const int window = i32(a[7]), sinks = i32(a[8]);
+  const float scale = scale_or_default(a[11], q.d);
+  void* stream = stream_of(a[1]);
+  const NoGil free;
   return attn_prefill_cache_window(q.q, c.k, c.v, c.lens, c.table, c.max_blocks, c.num_blocks, c.capacity, q.o,
-                                   q.o_type, q.lse, q.B, q.T, q.Hq, c.Hkv, q.d, scale_or_default(a[11], q.d),
-                                   i32(a[7]), i32(a[8]), stream_of(a[1]));
+                                   q.o_type, q.lse, q.B, q.T, q.Hq, c.Hkv, q.d, scale, window, sinks, stream);
 }
 
 // (dev, stream, q, k_cache, v_cache, k_scale, v_scale, seqlens, o, window, sinks, lse, page_table, max_seqlen_k,
@@ -228,6 +240,7 @@ int decode_window(PyObject* const* a) {
   const int window = i32(a[9]), sinks = i32(a[10]), longest = i32(a[13]), splits = i32(a[15]);
   const float scale = scale_or_default(a[14], q.d);
   void* stream = stream_of(a[1]);
+  const NoGil free;
   if (c.fp8)
     return attn_decode_window_fp8(q.q, c.k, c.v, c.k_scale, c.v_scale, c.lens, c.table, c.max_blocks, c.num_blocks,
                                   c.capacity, longest, q.o, q.o_type, q.lse, q.B, q.T, q.Hq, c.Hkv, q.d, scale, window,
@@ -252,6 +265,7 @@ int decode_shared(PyObject* const* a) {
   const int longest = i32(a[12]), causal = truth(a[14]), splits = i32(a[15]);
   const float scale = scale_or_default(a[13], q.d);
   void* stream = stream_of(a[1]);
+  const NoGil free;
   if (c.fp8)
     return attn_decode_shared_fp8(q.q, c.k, c.v, c.k_scale, c.v_scale, c.lens, c.table, c.max_blocks, c.num_blocks,
                                   pre, n, longest, q.o, q.o_type, q.lse, q.B, q.T, q.Hq, c.Hkv, q.d, scale, causal,
@@ -273,9 +287,13 @@ int norm_rope(PyObject* const* a) {
   const int32_t* pos0 = static_cast<int32_t*>(optional(a[11], "pos0", at::kInt, dev));
   if (pos0 && (THPVariable_Unpack(a[11]).dim() != 1 || THPVariable_Unpack(a[11]).size(0) != B))
     refuse("pos0 must be [B]");
-  return qk_norm_rope(q.p, k.p, q.stride, k.stride, typed(a[4], "q_out", at::kBFloat16, dev),
-                      typed(a[5], "k_out", at::kBFloat16, dev), t.qw, t.kw, real(a[9]), t.rope, t.rows, t.rot,
-                      truth(a[10]), pos0, B, T, Hq, dim(tk.size(2)), d, stream_of(a[1]));
+  void *q_out = typed(a[4], "q_out", at::kBFloat16, dev), *k_out = typed(a[5], "k_out", at::kBFloat16, dev);
+  const int Hkv = dim(tk.size(2)), interleaved = truth(a[10]);
+  const float eps = real(a[9]);
+  void* stream = stream_of(a[1]);
+  const NoGil free;
+  return qk_norm_rope(q.p, k.p, q.stride, k.stride, q_out, k_out, t.qw, t.kw, eps, t.rope, t.rows, t.rot, interleaved,
+                      pos0, B, T, Hq, Hkv, d, stream);
 }
 
 // (dev, stream, k_cache, v_cache, q, k_new, v_new, q_out, k_scale, v_scale, rope, cache_lens, page_table, q_weight,
@@ -294,6 +312,7 @@ int append_norm_rope(PyObject* const* a) {
   const float eps = real(a[15]);
   const int interleaved = truth(a[16]);
   void* stream = stream_of(a[1]);
+  const NoGil free;
   if (c.fp8)
     return kv_append_norm_rope_fp8(c.k, c.v, q.p, k.p, v.p, q.stride, k.stride, v.stride, q_out, c.k_scale, c.v_scale,
                                    t.qw, t.kw, eps, t.rope, t.rows, t.rot, interleaved, c.lens, c.table, c.max_blocks,

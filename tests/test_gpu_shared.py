@@ -261,3 +261,67 @@ def test_serving_step_of_forked_sequences(fp8):
             kv.attn_decode_window(q_out, kp, vp, to_dev_i32(lens), o, 20, 4, lse=lse, page_table=table)
         check(o, lse, serving.attention_window(qh, kc, vc, d ** -0.5, lens, 20, 4),
               serving.attention_window(qh, kc, np.abs(vc), d ** -0.5, lens, 20, 4)[0], f"window step {i}")
+
+
+def test_serving_steps_in_one_graph():
+    """Norm-rotate-append, then attention over a window and over the shared prefix, captured once and
+    replayed while the lengths grow on the device: each call sees what the one before it wrote."""
+    B, Hq, Hkv, d, prefix_blocks, steps, window, sinks = 5, 8, 2, 128, 40, 6, 700, 4
+    own = [1, 16, 31, 100, 900]
+    q, kp, vp, _, _, table, lens = make(B, 1, Hkv, Hq, d, prefix_blocks, [L + steps for L in own], seed=21)
+    lens = [16 * prefix_blocks + L for L in own]
+    qkv = torch.empty(B, 1, (Hq + 2 * Hkv) * d, dtype=torch.bfloat16, device="cuda")
+    qn, kn, vn = [x.unflatten(-1, (-1, d)) for x in qkv.split([Hq * d, Hkv * d, Hkv * d], dim=-1)]
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    rope, at, n = kv.rope_table(4096, d), to_dev_i32(lens), to_dev_i32([L + 1 for L in lens])
+    t, p = to_dev_i32(table), to_dev_i32(table[0, :prefix_blocks])
+    q_out = torch.empty(B, 1, Hq, d, dtype=torch.bfloat16, device="cuda")
+    o = [torch.empty(B, 1, Hq, d, device="cuda") for _ in range(2)]
+    lse = [torch.empty(B, Hq, 1, device="cuda") for _ in range(2)]
+    most = max(lens) + steps
+    ws = kv.decode_window_workspace(B, 1, Hq, Hkv, d, most, window, sinks)
+    ws2 = kv.decode_shared_workspace(B, 1, Hq, Hkv, d, most, prefix_blocks)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kv.kv_append_norm_rope(kp, vp, qn, kn, vn, q_out, rope, at, page_table=t, q_weight=w, k_weight=w)
+        kv.attn_decode_window(q_out, kp, vp, n, o[0], window, sinks, lse=lse[0], page_table=t, max_seqlen_k=most,
+                              workspace=ws)
+        kv.attn_decode_shared(q_out, kp, vp, n, t, p, o[1], lse=lse[1], max_seqlen_k=most, workspace=ws2)
+        at.add_(1)
+        n.add_(1)
+    for step in range(steps):
+        qkv.normal_()
+        g.replay()
+        torch.cuda.synchronize()
+        now = [L + step + 1 for L in lens]
+        pos = np.asarray(now)[:, None] - 1
+        qr = serving.norm_rotate(f64(qn), np.ones(d), 1e-6, pos, d)
+        assert np.abs(f64(q_out) - qr).max() <= (2.0 ** -8 + 2.0 ** -16) * np.abs(qr).max()
+        kc, vc = (oracle.gather_paged(f64(x), table, now) for x in (kp, vp))
+        new = serving.norm_rotate(f64(kn), np.ones(d), 1e-6, pos, d)[:, 0]
+        for b in range(B):
+            assert np.abs(kc[b, now[b] - 1] - new[b]).max() <= (2.0 ** -8 + 2.0 ** -16) * np.abs(new[b]).max()
+            assert np.array_equal(vc[b, now[b] - 1], f64(vn)[b, 0])
+        qh = f64(q_out)
+        check(o[0], lse[0], serving.attention_window(qh, kc, vc, d ** -0.5, now, window, sinks),
+              serving.attention_window(qh, kc, np.abs(vc), d ** -0.5, now, window, sinks)[0], f"window, step {step}")
+        check(o[1], lse[1], oracle.decode(qh, kc, vc, now, d ** -0.5, True),
+              oracle.decode(qh, kc, np.abs(vc), now, d ** -0.5, True)[0], f"shared, step {step}")
+
+
+def test_shared_prefix_on_two_streams():
+    """Two calls in flight, each with a workspace of its own."""
+    args = [make(6, 1, 2, 8, 128, 60, [5, 300, 64, 20, 900, 1], seed=s) for s in (31, 32)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    bufs = []
+    for q, kp, vp, _, _, table, lens in args:
+        bufs.append((to_dev_i32(lens), to_dev_i32(table), to_dev_i32(table[0, :60]), torch.empty(6, 1, 8, 128, device="cuda"),
+                     torch.empty(6, 8, 1, device="cuda"), kv.decode_shared_workspace(6, 1, 8, 2, 128, max(lens), 60)))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (q, kp, vp, *_), (n, t, p, o, lse, ws), s in zip(args, bufs, streams):
+            kv.attn_decode_shared(q, kp, vp, n, t, p, o, lse=lse, max_seqlen_k=16 * 60 + 900, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for a, (_, _, _, o, lse, _) in zip(args, bufs):
+        ref, weight = reference(*a, 128 ** -0.5)
+        check(o, lse, ref, weight)

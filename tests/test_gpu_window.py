@@ -156,6 +156,15 @@ def test_decode_window_many_sequences_balanced_and_not():
         parity(8, 8, 2, 128, 100, 4, lens, "paged", seed=90)
 
 
+@pytest.mark.parametrize("kind,T,Hq", [("paged", 1, 4), ("contig", 3, 8), ("fp8", 1, 4), ("fp8", 5, 8)])
+def test_decode_window_many_sequences_even_shares_and_not(kind, T, Hq):
+    """The warp-level forms with 128 sequences (even shares of the tiles) and 129 (chunks), a window too
+    long for one CTA per sequence; the latter's short ones have a share of a tile or two."""
+    for B in (128, 129):
+        lens = [T + 37 * (i % 50) ** 2 % 3000 for i in range(B)]
+        parity(T, Hq, 2, 128, 2900, 7, lens, kind, seed=91)
+
+
 @pytest.mark.parametrize("kind", ["contig", "paged", "fp8"])
 @pytest.mark.parametrize("T,Hq,Hkv", [(1, 8, 2), (8, 16, 2)])
 def test_wide_window_is_plain_decode(kind, T, Hq, Hkv):
