@@ -349,6 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* item_slot = reinterpret_cast<volatile int*>(tmem_slot + 2);
   int* order_smem = reinterpret_cast<int*>(smem + C::kOrderOff);
   const int* order = (!kDenseKv<KV> && p.B <= C::kMaxOrdered) ? order_smem : nullptr;
+  if constexpr (WIN) grid_dependency_wait();   // launched while the kernel before ends
   if (order) {
     // rank of each sequence by length, longest first (ties by index)
     for (int bb = threadIdx.x; bb < p.B; bb += blockDim.x) {
@@ -1007,6 +1008,7 @@ cudaError_t run_prefill(const PrefillLaunch& a, cudaStream_t stream) {
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const int grid = p.n_items < sms ? p.n_items : sms;
+  if constexpr (WIN) return launch_beside(kern, dim3(grid), kThreads, C::kSmemBytes, stream, true, tq, tk, tv, p);
   kern<<<grid, kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }
