@@ -65,7 +65,7 @@ ROT = [(128, 128, False), (128, 64, False), (128, 128, True), (128, 48, True), (
 
 
 @pytest.mark.parametrize("d,rot,interleaved", ROT)
-@pytest.mark.parametrize("B,T,Hq,Hkv", [(1, 1, 1, 1), (3, 5, 6, 2), (2, 33, 8, 8)])
+@pytest.mark.parametrize("B,T,Hq,Hkv", [(1, 1, 1, 1), (3, 5, 6, 2), (2, 33, 8, 8), (3, 1333, 9, 2), (3, 4099, 9, 2)])
 def test_qk_norm_rope_parity(d, rot, interleaved, B, T, Hq, Hkv):
     start = [0, 7, 100000][:B]
     rope = kv.rope_table(max(start) + T, rot) if rot else None
@@ -145,10 +145,13 @@ def cache_for(kind, lens, T, Hkv, d, seed):
 
 @pytest.mark.parametrize("kind", ["contig", "paged", "fp8", "fp8contig"])
 @pytest.mark.parametrize("d,rot,interleaved", [(128, 128, False), (64, 32, True)])
-@pytest.mark.parametrize("T", [1, 4, 37])
+@pytest.mark.parametrize("T", [1, 4, 37, 1501, 3203])
 def test_append_norm_rope_parity(kind, d, rot, interleaved, T):
-    """q_out and the new rows are right and nothing else of the cache changes."""
+    """q_out and the new rows are right and nothing else of the cache changes; few tokens and many (one,
+    two and four per warp), whole groups of them or not."""
     Hq, Hkv, lens = 6, 2, [0, 1, 15, 16, 300]
+    if T > 1000:
+        Hq, lens = (18, [0, 16, 301]) if d == 64 else (6, [1, 16, 301])
     B = len(lens)
     fp8 = kind.startswith("fp8")
     case = synth.decode_inputs(B, T, Hkv, Hkv, d, 0, 0, seed=20 + T, device="cuda", paged=kind in ("paged", "fp8"),
@@ -179,21 +182,21 @@ def test_append_norm_rope_parity(kind, d, rot, interleaved, T):
     else:
         kv.kv_append(k2, v2, k.contiguous(), v.contiguous(), at, page_table=table)
     assert torch.equal(vc, v2)
-    new = torch.zeros_like(kc, dtype=torch.bool)
+    new = torch.zeros(kc.shape[:2], dtype=torch.bool, device="cuda")
     for b in range(B):
-        for t in range(T):
-            p = lens[b] + t
-            row = (int(case.page_table[b, p // 16]), p % 16) if case.paged else (b, p)
-            new[row] = True
-            got = kc[row].cpu()
-            if fp8:
-                s = np.float64(case.k_scale)[:, None]
-                y = ofp8.e4m3_decode(got.numpy()) * s
-                want = np.clip(k_ref[b, t], -448 * s, 448 * s)
-                limit = (tol[b, t] - 2.0 ** -8 * np.abs(k_ref[b, t])) + 2.0 ** -4 * np.abs(want) * 1.001 + 2.0 ** -10 * s
-            else:
-                y, want, limit = f64(got), k_ref[b, t], tol[b, t]
-            assert (np.abs(y - want) <= limit).all(), (b, t)
+        p = torch.arange(lens[b], lens[b] + T)
+        row = (torch.as_tensor(case.page_table[b])[p // 16].long(), p % 16) if case.paged else (torch.full_like(p, b), p)
+        row = tuple(r.cuda() for r in row)
+        new[row] = True
+        got = kc[row].cpu()
+        if fp8:
+            s = np.asarray(case.k_scale, np.float64)[:, None]
+            y = ofp8.e4m3_decode(got.numpy()) * s
+            want = np.clip(k_ref[b], -448 * s, 448 * s)
+            limit = (tol[b] - 2.0 ** -8 * np.abs(k_ref[b])) + 2.0 ** -4 * np.abs(want) * 1.001 + 2.0 ** -10 * s
+        else:
+            y, want, limit = f64(got), k_ref[b], tol[b]
+        assert (np.abs(y - want) <= limit).all(), b
     assert torch.equal(kc[~new], before[0][~new])
 
 

@@ -156,6 +156,14 @@ def test_decode_window_many_sequences_balanced_and_not():
         parity(8, 8, 2, 128, 100, 4, lens, "paged", seed=90)
 
 
+@pytest.mark.parametrize("kind,T,Hq,Hkv,d", [("paged", 1, 150, 150, 64), ("contig", 1, 128, 1, 128), ("paged", 3, 128, 1, 64),
+                                             ("fp8", 1, 40, 1, 128), ("fp8", 2, 128, 1, 128), ("contig", 1, 1, 1, 64)])
+@pytest.mark.parametrize("window,sinks", [(90, 3), (2500, 40)])
+def test_decode_window_head_layouts(kind, T, Hq, Hkv, d, window, sinks):
+    """More KV heads than SMs, up to 128 query heads of one KV head (several row tiles), a single head."""
+    parity(T, Hq, Hkv, d, window, sinks, [3, 70, 2700, 4001], kind, seed=95)
+
+
 @pytest.mark.parametrize("kind,T,Hq", [("paged", 1, 4), ("contig", 3, 8), ("fp8", 1, 4), ("fp8", 5, 8)])
 def test_decode_window_many_sequences_even_shares_and_not(kind, T, Hq):
     """The warp-level forms with 128 sequences (even shares of the tiles) and 129 (chunks), a window too
