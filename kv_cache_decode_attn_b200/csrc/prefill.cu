@@ -46,7 +46,7 @@
 // the keys from its first row's window on (rounded down to a 16-token block), so a tile
 // is one run of positions, an item's work is about window + 256 keys whatever its
 // position, and masks and limits work on the numbers.  Query tile B leaves out the
-// window tiles that only tile A's rows see.  With up to 64 first tokens their tile is a
+// window tiles that only tile A's rows see, and everything where it has no rows.  With up to 64 first tokens their tile is a
 // narrow one: MMAs and softmax over just those columns.  4096-token prompts with a window
 // of 1024 and 4 first tokens: 11 and 10 tiles per item of two query tiles without the
 // last two points, 9 and a narrow one each with them.
@@ -201,7 +201,8 @@ struct Item {
   bool bad;                      // invalid length (cached forms): the rows are written as NaN
   // WIN: L and off count the item's numbered keys; the tiles below s_tiles hold the first
   // tokens, a number v from there on is position v + gap; query tile B's rows see the tiles
-  // below s_tiles and from jb on; cols < kBN: the first tile is narrow
+  // below s_tiles and from jb on, or it has no rows (empty_b); cols < kBN: the first tile is narrow
+  bool empty_b;
   int s_tiles, gap, w0, jb, cols;   // w0: first position read past the first tokens
 };
 
@@ -233,6 +234,7 @@ __device__ __forceinline__ Item item_of(int w, const PrefillParams& p, const int
   }
   it.s_tiles = it.gap = it.w0 = it.jb = 0;
   it.cols = kBN;
+  it.empty_b = false;
   if constexpr (WIN) {
     int L = p.N;
     it.bad = false;
@@ -251,6 +253,8 @@ __device__ __forceinline__ Item item_of(int w, const PrefillParams& p, const int
     const int nt = (it.L + kBN - 1) / kBN;
     it.n_kv0 = min((it.off + 2 * it.qb * kBM + kBM + kBN - 1) / kBN, nt);
     it.n_load = min((it.off + 2 * it.qb * kBM + 2 * kBM + kBN - 1) / kBN, nt);
+    it.empty_b = (2 * it.qb + 1) * kBM >= p.N;
+    if (it.empty_b) it.n_load = it.n_kv0;
     it.jb = min(max(max(0, row0 + kBM - p.window + 1 - it.gap) / kBN, it.s_tiles), it.n_load - 1);
     const int s16 = (p.sinks + kPageTokens - 1) & ~(kPageTokens - 1);
     if (it.gap > 0 && s16 > 0 && s16 <= kNarrow) it.cols = s16;
@@ -619,7 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int s_tiles = WIN ? __shfl_sync(0xffffffffu, itm.s_tiles, 0) : 0;
       const int jb = WIN ? __shfl_sync(0xffffffffu, itm.jb, 0) : 0;
       const int cols = WIN ? __shfl_sync(0xffffffffu, itm.cols, 0) : kBN;
-      auto sees_b = [&](int j) { return !WIN || j < s_tiles || j >= jb; };
+      const bool empty_b = WIN && __shfl_sync(0xffffffffu, (int)itm.empty_b, 0) != 0;
+      auto sees_b = [&](int j) { return !WIN || (!empty_b && (j < s_tiles || j >= jb)); };
       const int n_keys = WIN ? __shfl_sync(0xffffffffu, itm.L, 0) : 0;
       const int dead_end = WIN ? __shfl_sync(0xffffffffu, itm.off + 2 * itm.qb * kBM, 0) + 1 - p.window : 0;
       bool first_b = true;
@@ -720,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (w < 0) break;                                   // no more work
     const Item itm = item_of<KV, WIN>(w, p, order);
     const int q_row = (2 * itm.qb + t) * kBM + row;
-    const int nkv = t ? itm.n_load : itm.n_kv0;
+    const int nkv = t ? (itm.empty_b ? 0 : itm.n_load) : itm.n_kv0;
     float m = -INFINITY, l = 0.f;
     const int j_first = WIN && t == 1 && itm.s_tiles == 0 ? itm.jb : 0;   // the group's first tile
     for (int j = j_first; j < nkv; ++j) {
