@@ -184,6 +184,7 @@ struct PrefillParams {
   int max_keys;                // cache capacity in tokens (contiguous) or max_blocks * 16 (paged)
   int max_blocks, num_blocks;
   int window, sinks;           // WIN instances
+  int item_tiles;              // WIN instances: query tiles per item, 2 or (too few items for the SMs) 1
 };
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
@@ -244,16 +245,17 @@ __device__ __forceinline__ Item item_of(int w, const PrefillParams& p, const int
       if (it.bad) L = p.N;             // a safe stand-in; the host checked p.N <= p.max_keys
     }
     it.s_tiles = (p.sinks + kBN - 1) / kBN;
-    const int row0 = L - p.N + 2 * it.qb * kBM;   // position of the item's first row
+    const int q0 = p.item_tiles * it.qb * kBM;
+    const int row0 = L - p.N + q0;                // position of the item's first row
     // block of the first key in that row's window
     it.w0 = max(0, row0 - p.window + 1) & ~(kPageTokens - 1);
     it.gap = max(0, it.w0 - it.s_tiles * kBN);
     it.L = L - it.gap;
     it.off = it.L - p.N;
     const int nt = (it.L + kBN - 1) / kBN;
-    it.n_kv0 = min((it.off + 2 * it.qb * kBM + kBM + kBN - 1) / kBN, nt);
-    it.n_load = min((it.off + 2 * it.qb * kBM + 2 * kBM + kBN - 1) / kBN, nt);
-    it.empty_b = (2 * it.qb + 1) * kBM >= p.N;
+    it.n_kv0 = min((it.off + q0 + kBM + kBN - 1) / kBN, nt);
+    it.n_load = min((it.off + q0 + 2 * kBM + kBN - 1) / kBN, nt);
+    it.empty_b = p.item_tiles == 1 || q0 + kBM >= p.N;
     if (it.empty_b) it.n_load = it.n_kv0;
     it.jb = min(max(max(0, row0 + kBM - p.window + 1 - it.gap) / kBN, it.s_tiles), it.n_load - 1);
     const int s16 = (p.sinks + kPageTokens - 1) & ~(kPageTokens - 1);
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int hh = 0; hh < C::kHalves; ++hh)
               tma_load_4d(smem + C::kQOff + t * C::kTileBytes + hh * C::kHalfBytes, &tmQ, &bars[B_QFULL], hh * 64,
-                          itm.h, (2 * itm.qb + t) * kBM, itm.b, once);
+                          itm.h, ((WIN ? p.item_tiles : 2) * itm.qb + t) * kBM, itm.b, once);
           if (w_next < p.n_items) {                 // warm L2 with the next item's Q
             const Item nx = item_of<KV, WIN>(w_next, p, order);
 #pragma unroll
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool empty_b = WIN && __shfl_sync(0xffffffffu, (int)itm.empty_b, 0) != 0;
       auto sees_b = [&](int j) { return !WIN || (!empty_b && (j < s_tiles || j >= jb)); };
       const int n_keys = WIN ? __shfl_sync(0xffffffffu, itm.L, 0) : 0;
-      const int dead_end = WIN ? __shfl_sync(0xffffffffu, itm.off + 2 * itm.qb * kBM, 0) + 1 - p.window : 0;
+      const int dead_end = WIN ? __shfl_sync(0xffffffffu, itm.off + p.item_tiles * itm.qb * kBM, 0) + 1 - p.window : 0;
       bool first_b = true;
       const int g0 = g;
       const int ks0 = g0 % kKStages;
@@ -724,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(&bars[B_QEMPTY]);        // this warp has read the item
     if (w < 0) break;                                   // no more work
     const Item itm = item_of<KV, WIN>(w, p, order);
-    const int q_row = (2 * itm.qb + t) * kBM + row;
+    const int q_row = ((WIN ? p.item_tiles : 2) * itm.qb + t) * kBM + row;
     const int nkv = t ? (itm.empty_b ? 0 : itm.n_load) : itm.n_kv0;
     float m = -INFINITY, l = 0.f;
     const int j_first = WIN && t == 1 && itm.s_tiles == 0 ? itm.jb : 0;   // the group's first tile
@@ -868,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const float inv_l = itm.bad ? __int_as_float(0x7fc00000) : 1.f / l;   // NaN rows for a bad length
       if (itm.bad && t == 0 && row == 0) atomicOr(p.status, DEV_SEQLEN);
-      const bool store = q_row < p.N;
+      const bool store = q_row < p.N && !(WIN && t && itm.empty_b);
       const size_t obase = (((size_t)itm.b * p.N + q_row) * p.Hq + itm.h) * D;
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
@@ -980,7 +982,13 @@ cudaError_t run_prefill(const PrefillLaunch& a, cudaStream_t stream) {
   p.Hkv = a.Hkv;
   p.G = a.Hq / a.Hkv;
   p.B = a.B;
-  p.n_qblocks = (a.N + 2 * kBM - 1) / (2 * kBM);
+  p.item_tiles = 2;
+  if constexpr (WIN) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if ((a.N + 2 * kBM - 1) / (2 * kBM) * (long long)a.Hq * a.B * 2 <= sms) p.item_tiles = 1;
+  }
+  p.n_qblocks = (a.N + p.item_tiles * kBM - 1) / (p.item_tiles * kBM);
   p.n_ktiles = (a.N + kBN - 1) / kBN;
   const long long items = (long long)p.n_qblocks * a.Hq * a.B;
   if (items > INT32_MAX) return cudaErrorInvalidValue;
