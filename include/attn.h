@@ -326,7 +326,9 @@ ATTN_API size_t attn_decode_shared_workspace_bytes(int B, int T, int Hq, int Hkv
  * samples).  The prefix's K and V are read once for the whole batch: the queries of
  * all sequences meet them as one tile of rows, each sequence's queries then meet
  * its own keys, and the two parts are merged by their log-sum-exps ([P3] "背景", the
- * stable reduction of partial softmax results).  Same result as attn_decode over
+ * stable reduction of partial softmax results).  With few sequences or a short prefix,
+ * where three launches would take longer, each sequence reads the prefix for itself
+ * (from L2 after the first; automatic num_splits only).  Same result as attn_decode over
  * tables whose first prefix_blocks entries are prefix_table's.
  *
  *   k_cache, v_cache  paged pools [num_blocks, 16, Hkv, d] (sharing needs pages)

@@ -452,7 +452,7 @@ def attn_decode_shared(q, k_cache, v_cache, seqlens_k, page_table, prefix_table,
     """``attn_decode`` over pools ``[nblk, 16, Hkv, d]`` for a batch whose sequences share their
     first blocks: prefix_table int32 ``[prefix_blocks]`` names them (``page_table[0, :n]`` serves)
     and page_table's first prefix_blocks columns are not read.  The prefix is read once for the
-    whole batch.  seqlens_k counts the prefix and the T new tokens."""
+    whole batch, or by each sequence where that is faster (few sequences, a short prefix).  seqlens_k counts the prefix and the T new tokens."""
     _decode_shared("attn_decode_shared", q, k_cache, v_cache, None, None, seqlens_k, page_table, prefix_table, o, lse,
                    max_seqlen_k, scale, causal, num_splits, workspace, stream)
 

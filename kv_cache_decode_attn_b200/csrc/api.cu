@@ -353,6 +353,7 @@ int decode_impl(const void* q, const void* k_cache, const void* v_cache, const f
 // Shared-prefix decode: the launches' parts of the workspace.  The prefix's partials are
 // those of one sequence with B * T query tokens; the own part's follow.
 struct SharedLayout {
+  int together;   // as if nothing were shared: own is the layout of the whole
   int pre_chunk, pre_chunks, pre_stream;
   size_t pre_lse_offset, own_offset, total;
   DecodeLayout own;
@@ -365,7 +366,14 @@ bool shared_layout(int B, int T, int Hq, int Hkv, int d, int max_seqlen_k, int p
   if ((long long)B * T > INT32_MAX / 128 || Hq / Hkv > 128) return false;
   const int P = prefix_blocks * kPageTokens;
   if (max_seqlen_k - P < T) return false;
-  SharedLayout s;
+  SharedLayout s = {};
+  if (num_splits == 0 && decode_shared_together(B, T, Hq / Hkv, Hkv, max_seqlen_k, P, fp8)) {
+    s.together = 1;
+    if (!decode_layout(B, T, Hq, Hkv, d, max_seqlen_k, 0, fp8, &s.own, true, true)) return false;
+    s.total = s.own.total;
+    *out = s;
+    return true;
+  }
   if (!decode_layout(B, T, Hq, Hkv, d, max_seqlen_k - P, num_splits, fp8, &s.own, true)) return false;
   const int R = B * T * (Hq / Hkv);   // the prefix's query rows per KV head
   s.pre_chunk = prefix_chunk_tokens(B * T, Hq / Hkv, Hkv, P, num_splits, fp8);
@@ -463,6 +471,14 @@ int shared_impl(const void* q, const void* k_cache, const void* v_cache, const f
   own.early = 0;
   own.fence = 1;
   own.sel.fixed_len = 0;
+  own.sel.min_len = prefix_blocks * kPageTokens + T;
+  if (s.together) {
+    own.direct = s.own.direct;
+    own.early = own.fence = 0;
+    own.sel.prefix = prefix_table;
+    own.sel.prefix_blocks = prefix_blocks;
+    return cuda_status(launch_decode(own, static_cast<cudaStream_t>(stream)), name);
+  }
   own.sel.skip = prefix_blocks * kPageTokens;
   own.pre_o = pre.part_o;
   own.pre_lse = pre.part_lse;

@@ -166,13 +166,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
 
   if (warp == C::kConsumerWarps) {
     // ------------------------------------------------------------ producer
-    if (SEL && p.stream) {
-      produce_stream<C, PAGED>(smem, full, empty, &tmK, &tmV, p, plan, stream_segment<PAGED>(p, plan, x, x1), x, x1,
-                               abort_flag);
-    } else if (lane == 0) {
-      produce_split_tiles<C, PAGED, SEL>(smem, full, empty, &tmK, &tmV, p, b, g, tok_begin, tok_end, n_tiles, sk,
-                                         abort_flag);
-    }
+    auto produce = [&](auto prefix) {
+      constexpr bool PREFIX = decltype(prefix)::value;
+      if (SEL && p.stream) {
+        produce_stream<C, PAGED, PREFIX>(smem, full, empty, &tmK, &tmV, p, plan,
+                                         stream_segment<PAGED>(p, plan, x, x1), x, x1, abort_flag);
+      } else if (lane == 0) {
+        produce_split_tiles<C, PAGED, SEL, PREFIX>(smem, full, empty, &tmK, &tmV, p, b, g, tok_begin, tok_end, n_tiles,
+                                                   sk, abort_flag);
+      }
+    };
+    if (SEL && PAGED && p.sel.prefix_blocks) produce(std::bool_constant<SEL && PAGED>{});
+    else produce(std::false_type{});
     return;
   }
 
@@ -994,6 +999,24 @@ bool decode_direct(long long units, int max_keys, bool tc) {
   const double tiles = (max_keys + kDecodeTile - 1) / kDecodeTile, sms = device_sms(), tile = tc ? 1.3 : 0.65;
   const double waves = units <= sms ? 1.0 : 1.7 * ceil(units / (2 * sms));
   return tiles * tile * waves <= tiles * 0.55 * units / sms + 5.0;
+}
+
+bool decode_shared_together(int B, int T, int G, int Hkv, int max_seqlen, int prefix, bool fp8) {
+  // us on B200, as in decode_direct (0.55 a tile with two CTAs per SM, 1.0 on the tensor-core kernel,
+  // 8 to start, split and merge), against the three launches of the shared form: 4 sequences behind
+  // 1024 tokens 11.1 us instead of 14.2, 40 behind 256 tokens 8.6 instead of 13.8.  Not on the
+  // tensor-core kernel: the lookup there slowed every shared call (94 to 99 us behind 32768 tokens).
+  const int rows = G * T;
+  if (decode_uses_tc(rows, fp8)) return false;
+  const double sms = device_sms();
+  auto share = [&](int rows, int row_tiles, double tiles) {
+    return tiles * row_tiles * Hkv * (decode_uses_tc(rows, fp8) ? 1.0 : 0.55) / sms;
+  };
+  const double all = (double)B * ((max_seqlen + kDecodeTile - 1) / kDecodeTile);
+  const double own = (double)B * ((max_seqlen - prefix + kDecodeTile - 1) / kDecodeTile);
+  const double pre = (prefix + kDecodeTile - 1) / kDecodeTile;
+  return share(rows, 1, all) + 8.0 <
+         share(rows, 1, own) + share(rows * B, decode_row_tiles(B * T, G), pre) + 13.0;
 }
 
 int decode_stream_ctas(int B, int R, int Hkv, int max_keys, bool fp8) {

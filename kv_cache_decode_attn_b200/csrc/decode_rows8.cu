@@ -131,12 +131,17 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
   }
 
   if (warp == C::kConsumerWarps) {
-    if (p.stream) {
-      produce_stream<C, PAGED>(smem, full, empty, &tmK, &tmV, p, &plan, sg, x, x1, abort_flag);
-    } else if (lane == 0) {
-      produce_split_tiles<C, PAGED, true>(smem, full, empty, &tmK, &tmV, p, sg.b, sg.g, sg.tok_begin, sg.tok_end,
-                                          sg.n_tiles, sg.sk, abort_flag);
-    }
+    auto produce = [&](auto prefix) {
+      constexpr bool PREFIX = decltype(prefix)::value;
+      if (p.stream) {
+        produce_stream<C, PAGED, PREFIX>(smem, full, empty, &tmK, &tmV, p, &plan, sg, x, x1, abort_flag);
+      } else if (lane == 0) {
+        produce_split_tiles<C, PAGED, true, PREFIX>(smem, full, empty, &tmK, &tmV, p, sg.b, sg.g, sg.tok_begin,
+                                                    sg.tok_end, sg.n_tiles, sg.sk, abort_flag);
+      }
+    };
+    if (PAGED && p.sel.prefix_blocks) produce(std::bool_constant<PAGED>{});
+    else produce(std::false_type{});
     return;
   }
 

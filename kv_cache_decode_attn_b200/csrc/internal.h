@@ -52,6 +52,10 @@ int decode_balanced_chunks(int B, int Hkv, int items_per_slot = kBalancedItemsPe
 // itself, rather than split them over the SMs and merge.  tc: the tensor-core kernel's.
 bool decode_direct(long long units, int max_keys, bool tc);
 
+// Whether a batch behind a shared prefix of `prefix` tokens is decoded as if it shared nothing
+// (each sequence reads the prefix, from L2 after the first), in one split and at most one merge.
+bool decode_shared_together(int B, int T, int G, int Hkv, int max_seqlen, int prefix, bool fp8);
+
 // Windowed and shared-prefix decode (the SEL instances) on the warp-level kernels, automatic
 // splitting: this many CTAs per KV head share its tiles evenly (0: too many sequences or tiles for it,
 // one CTA per chunk then).
@@ -69,6 +73,10 @@ struct KeySelect {
   int window = kMaxDecodeSeqlen;   // at most that, so that position - window - position stays inside int
   int sinks = 0;
   int skip = 0;        // > 0: only the keys from position skip (a multiple of 16) on
+  int min_len = 0;     // shorter sequences are invalid
+  // the first prefix_blocks blocks of every sequence are these, whatever its page-table row says
+  const int32_t* prefix = nullptr;
+  int prefix_blocks = 0;
   int fixed_len = 0;   // > 0: every sequence has exactly this many keys (seqlens is not read)
 };
 

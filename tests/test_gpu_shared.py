@@ -98,6 +98,42 @@ def test_shared_prefix_parity(fp8, B, T, Hq, Hkv, d, prefix_blocks, own):
         check(o, lse, ref, weight, f"B={B} T={T}")
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,T,Hq,Hkv,d,prefix_blocks,own", [
+    (24, 1, 8, 2, 128, 400, [1 + 13 * i for i in range(24)]),          # 96 prefix rows: the tensor-core kernel
+    (20, 2, 16, 2, 128, 300, [2 + 7 * i for i in range(20)]),          # 320 rows: several row tiles, 16 own rows
+    (5, 1, 6, 2, 128, 1500, [1, 16, 17, 100, 640]),                    # 15 rows: the warp-level kernels
+    (2, 1, 8, 2, 128, 4000, [5, 300]),                                 # 8 rows
+    (30, 1, 4, 2, 64, 500, [1 + 29 * i for i in range(30)]),
+    (20, 8, 16, 2, 128, 300, [8 + 31 * i for i in range(20)]),         # 64 own rows: tensor cores there too
+])
+def test_long_shared_prefix_parity(fp8, B, T, Hq, Hkv, d, prefix_blocks, own):
+    """Prefixes long enough that they are read once for the batch (short ones are read by each sequence)."""
+    if fp8 and d != 128:
+        pytest.skip("FP8 caches are built for d = 128")
+    args = make(B, T, Hkv, Hq, d, prefix_blocks, own, seed=200 + B, fp8=fp8)
+    ref, weight = reference(*args, 1.0 / math.sqrt(d))
+    for causal in (True, False):
+        o, lse = call(*args, prefix_blocks, causal=causal)
+        if not causal:
+            ref, weight = reference(*args, 1.0 / math.sqrt(d), False)
+        check(o, lse, ref, weight, f"B={B} T={T} causal={causal}")
+    # a length short of prefix + T, and a block outside the pool
+    lens = list(args[6])
+    short = list(args)
+    short[6] = [16 * prefix_blocks + T - 1] + lens[1:]
+    o, lse = call(*short, prefix_blocks, causal=False)
+    assert kv.attn_get_device_status(clear=True) == kv.ATTN_DEV_SEQLEN
+    assert torch.isnan(o[0]).all() and torch.isnan(lse[0]).all()
+    check(o[1:], lse[1:], (ref[0][1:], ref[1][1:]), weight[1:])
+    table = args[5].copy()
+    table[0, prefix_blocks // 2] = -7
+    bad = list(args)
+    bad[5] = table
+    call(*bad, prefix_blocks)
+    assert kv.attn_get_device_status(clear=True) == kv.ATTN_DEV_PAGE_ID
+
+
 @pytest.mark.parametrize("num_splits", [1, 3, 40])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("fp8", [False, True])
@@ -154,12 +190,13 @@ def test_shared_prefix_bad_scale_is_flagged():
     assert torch.isnan(o[:, :, :4]).all() and not torch.isnan(o[:, :, 4:]).any()
 
 
-def test_shared_prefix_replays_in_a_graph():
-    args = make(5, 1, 2, 8, 128, 30, [9, 100, 64, 20, 300], seed=12)
+@pytest.mark.parametrize("blocks", [30, 1200])   # read by each sequence, and once for the batch
+def test_shared_prefix_replays_in_a_graph(blocks):
+    args = make(5, 1, 2, 8, 128, blocks, [9, 100, 64, 20, 300], seed=12)
     q, kp, vp, _, _, table, lens = args
-    t, p, n = to_dev_i32(table), to_dev_i32(table[0, :30]), to_dev_i32(lens)
+    t, p, n = to_dev_i32(table), to_dev_i32(table[0, :blocks]), to_dev_i32(lens)
     o, lse = torch.empty(5, 1, 8, 128, device="cuda"), torch.empty(5, 8, 1, device="cuda")
-    ws = kv.decode_shared_workspace(5, 1, 8, 2, 128, max(lens), 30)
+    ws = kv.decode_shared_workspace(5, 1, 8, 2, 128, max(lens), blocks)
 
     def go():
         kv.attn_decode_shared(q, kp, vp, n, t, p, o, lse=lse, max_seqlen_k=max(lens), workspace=ws)
