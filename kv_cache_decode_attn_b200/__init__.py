@@ -13,6 +13,7 @@ The raw ctypes handle is ``lib``; tests call through it or through these wrapper
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -148,6 +149,17 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _allocating_on(stream, device):
+    """Where a call allocates for itself: on the stream that it launches on, so that the memory goes back to
+    that stream and no other gets it while the kernels use it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -242,7 +254,8 @@ def _cache_geometry(k_cache, page_table):
 def attn_decode(q, k_cache, v_cache, seqlens_k, o, lse=None, page_table=None, max_seqlen_k=0, scale=None,
                 causal=True, num_splits=0, workspace=None, stream=None) -> None:
     """q ``[B, T, Hq, d]``; k/v cache ``[B, cap, Hkv, d]`` or pools ``[nblk, 16, Hkv, d]``;
-    seqlens_k int32 ``[B]`` (including the T new tokens); page_table int32 ``[B, max_blocks]``."""
+    seqlens_k int32 ``[B]`` (including the T new tokens); page_table int32 ``[B, max_blocks]``.
+    Without a workspace the call takes one from torch's pool of the stream it runs on."""
     B, T, Hq, d = q.shape
     max_blocks, num_blocks, cap, Hkv = _cache_geometry(k_cache, page_table)
     if tuple(v_cache.shape) != tuple(k_cache.shape) or tuple(o.shape) != (B, T, Hq, d):
@@ -252,7 +265,8 @@ def attn_decode(q, k_cache, v_cache, seqlens_k, o, lse=None, page_table=None, ma
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     if workspace is None:
         msk = max_seqlen_k if max_seqlen_k else (cap if page_table is None else max_blocks * 16)
-        workspace = decode_workspace(B, T, Hq, Hkv, d, msk, num_splits, q.device)
+        with _allocating_on(stream, q.device):
+            workspace = decode_workspace(B, T, Hq, Hkv, d, msk, num_splits, q.device)
     st = lib.attn_decode(_dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache", torch.bfloat16),
                          _dev(v_cache, "v_cache", torch.bfloat16), _dev(seqlens_k, "seqlens_k", torch.int32),
                          None if page_table is None else _dev(page_table, "page_table", torch.int32),
@@ -323,7 +337,8 @@ def attn_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, seqlens_k, o, lse=Non
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     if workspace is None:
         msk = max_seqlen_k if max_seqlen_k else (cap if page_table is None else max_blocks * 16)
-        workspace = decode_workspace(B, T, Hq, Hkv, d, msk, num_splits, q.device)
+        with _allocating_on(stream, q.device):
+            workspace = decode_workspace(B, T, Hq, Hkv, d, msk, num_splits, q.device)
     st = lib.attn_decode_fp8(_dev(q, "q", torch.bfloat16), _codes(k_cache, "k_cache"), _codes(v_cache, "v_cache"),
                              _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32),
                              _dev(seqlens_k, "seqlens_k", torch.int32),
@@ -397,9 +412,10 @@ def attn_decode_window(q, k_cache, v_cache, seqlens_k, o, window, sinks=0, lse=N
     j <= p with j > p - window or j < sinks.  Only the blocks holding such keys are read."""
     here = _here(q, stream)
     if workspace is None:
-        workspace = decode_window_workspace(*q.shape[:3], k_cache.shape[2], q.shape[3],
-                                            _longest(k_cache, page_table, max_seqlen_k), window, sinks, num_splits,
-                                            q.device)
+        with _allocating_on(stream, q.device):
+            workspace = decode_window_workspace(*q.shape[:3], k_cache.shape[2], q.shape[3],
+                                                _longest(k_cache, page_table, max_seqlen_k), window, sinks, num_splits,
+                                                q.device)
     st = _marshal.decode_window(*here, q, k_cache, v_cache, None, None, seqlens_k, o, window, sinks, lse, page_table,
                                 max_seqlen_k, scale, num_splits, workspace)
     _check("attn_decode_window", st)
@@ -411,9 +427,10 @@ def attn_decode_window_fp8(q, k_cache, v_cache, k_scale, v_scale, seqlens_k, o, 
     """``attn_decode_window`` over an FP8 cache (arguments as ``attn_decode_fp8``)."""
     here = _here(q, stream)
     if workspace is None:
-        workspace = decode_window_workspace(*q.shape[:3], k_cache.shape[2], q.shape[3],
-                                            _longest(k_cache, page_table, max_seqlen_k), window, sinks, num_splits,
-                                            q.device)
+        with _allocating_on(stream, q.device):
+            workspace = decode_window_workspace(*q.shape[:3], k_cache.shape[2], q.shape[3],
+                                                _longest(k_cache, page_table, max_seqlen_k), window, sinks, num_splits,
+                                                q.device)
     st = _marshal.decode_window(*here, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, o, window, sinks, lse,
                                 page_table, max_seqlen_k, scale, num_splits, workspace)
     _check("attn_decode_window_fp8", st)
@@ -439,9 +456,10 @@ def _decode_shared(name, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_
     if workspace is None:
         if page_table is None:
             raise ValueError("a shared prefix needs a page table")
-        workspace = decode_shared_workspace(*q.shape[:3], k_cache.shape[2], q.shape[3],
-                                            _longest(k_cache, page_table, max_seqlen_k), prefix_table.shape[0],
-                                            num_splits, q.device)
+        with _allocating_on(stream, q.device):
+            workspace = decode_shared_workspace(*q.shape[:3], k_cache.shape[2], q.shape[3],
+                                                _longest(k_cache, page_table, max_seqlen_k), prefix_table.shape[0],
+                                                num_splits, q.device)
     st = _marshal.decode_shared(*here, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_table, prefix_table, o,
                                 lse, max_seqlen_k, scale, causal, num_splits, workspace)
     _check(name, st)
@@ -477,8 +495,10 @@ def rope_table_fill(table, theta=10000.0, stream=None) -> None:
 
 
 def rope_table(rows, rot_dim, theta=10000.0, device="cuda", stream=None) -> torch.Tensor:
-    """A new angle table for positions 0 .. rows - 1 (``rope_table_fill``)."""
-    table = torch.empty(int(rows), int(rot_dim), dtype=torch.float32, device=device)
+    """A new angle table for positions 0 .. rows - 1 (``rope_table_fill``), allocated and filled on
+    ``stream``: like any tensor made there, other streams wait for it before they use it."""
+    with _allocating_on(stream, device):
+        table = torch.empty(int(rows), int(rot_dim), dtype=torch.float32, device=device)
     rope_table_fill(table, theta, stream)
     return table
 

@@ -1,0 +1,75 @@
+"""GPU tests of what the calls do at the edges of their arguments and of how they are used."""
+
+import pytest
+import torch
+
+import synth
+
+pytestmark = pytest.mark.gpu
+
+kv = pytest.importorskip("kv_cache_decode_attn_b200")
+from tests.gpu_util import to_dev_i32  # noqa: E402
+
+
+@pytest.fixture(autouse=True)
+def _need_cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    kv.attn_get_device_status(clear=True)
+    yield
+    assert kv.attn_get_device_status(clear=True) == 0
+
+
+# ------------------------------------------------------------------------------- streams of their own
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_calls_on_another_stream_make_their_own_workspace_there(as_handle):
+    """Launched on a stream that is held up, without a workspace, while the current stream allocates and
+    writes: the outputs are those of a call with a workspace of its own."""
+    B, Hq, Hkv, d, blocks = 4, 32, 8, 128, 80
+    lens = [16 * blocks + n for n in (5, 300, 64, 900)]
+    case = synth.decode_inputs(B, 1, Hq, Hkv, d, 0, 0, seed=3, device="cuda", paged=True, lengths=[L - 1 for L in lens])
+    fp8 = synth.decode_inputs(B, 1, Hq, Hkv, d, 0, 0, seed=4, device="cuda", paged=True, lengths=[L - 1 for L in lens],
+                              fp8=True)
+    t, n, most = to_dev_i32(case.page_table), to_dev_i32(lens), max(lens)
+    t8 = to_dev_i32(fp8.page_table)
+    t[:, :blocks], t8[:, :blocks] = t[0, :blocks].clone(), t8[0, :blocks].clone()
+    p, p8 = t[0, :blocks].contiguous(), t8[0, :blocks].contiguous()
+    bf, e4 = (case.q, case.k_pool, case.v_pool), (fp8.q, fp8.k_pool, fp8.v_pool)
+    scales = [torch.as_tensor(s, device="cuda") for s in (fp8.k_scale, fp8.v_scale)]
+    sizes = (B, 1, Hq, Hkv, d, most)
+    plain, window = kv.decode_workspace(*sizes), kv.decode_window_workspace(*sizes, 900, 4)
+    shared = kv.decode_shared_workspace(*sizes, blocks)
+    calls = [
+        (plain, lambda o, **kw: kv.attn_decode(*bf, n, o, page_table=t, max_seqlen_k=most, **kw)),
+        (plain, lambda o, **kw: kv.attn_decode_fp8(*e4, *scales, n, o, page_table=t8, max_seqlen_k=most, **kw)),
+        (window, lambda o, **kw: kv.attn_decode_window(*bf, n, o, 900, 4, page_table=t, max_seqlen_k=most, **kw)),
+        (window, lambda o, **kw: kv.attn_decode_window_fp8(*e4, *scales, n, o, 900, 4, page_table=t8, max_seqlen_k=most,
+                                                           **kw)),
+        (shared, lambda o, **kw: kv.attn_decode_shared(*bf, n, t, p, o, max_seqlen_k=most, **kw)),
+        (shared, lambda o, **kw: kv.attn_decode_shared_fp8(*e4, *scales, n, t8, p8, o, max_seqlen_k=most, **kw)),
+    ]
+    side = torch.cuda.Stream()
+    for ws, call in calls:
+        want, got = torch.empty(B, 1, Hq, d, device="cuda"), torch.empty(B, 1, Hq, d, device="cuda")
+        call(want, workspace=ws)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        call(got, stream=side.cuda_stream if as_handle else side)
+        taken = [torch.full_like(ws, 0xFF) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        assert all(bool((x == 0xFF).all()) for x in taken)
+
+
+def test_an_angle_table_made_on_another_stream():
+    want = kv.rope_table(3000, 128)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    del_me = torch.full((3000, 128), 7.0, device="cuda")     # written late, its memory free at once
+    del del_me
+    got = kv.rope_table(3000, 128, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
