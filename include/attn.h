@@ -492,9 +492,8 @@ ATTN_API int attn_selftest_wait_timeout(void* stream);
  *     layouts, so it can exceed what this call needs); a smaller num_splits
  *     needs less.
  *   - The array's device address is looked up once per device and kept for the
- *     life of the process; like the library's status word and work-queue
- *     counters it does not survive cudaDeviceReset or the destruction of the
- *     device's primary context.
+ *     life of the process; like the library's status word it does not survive
+ *     cudaDeviceReset or the destruction of the device's primary context.
  */
 #define ATTN_DECODE_NOALLOC_SCRATCH_BYTES (32u << 20) /* 32 MiB */
 

@@ -1,15 +1,16 @@
 // Prefill attention on the sm_100a tensor cores (tcgen05 + TMEM + TMA).
 //
-// Persistent: one CTA per SM takes work items from a queue, heaviest causal
-// query blocks first (its first item is its block index; every further item is
-// a ticket from a global counter, so a CTA that finishes early takes more
-// work instead of waiting on a fixed share).  A work item is two 128-row query tiles (A: rows 256*qb .. +127,
+// The grid has a CTA per work item, heaviest causal query blocks first, of which one
+// per SM runs; each goes on with the items of CTAs that have not started (cluster launch
+// control takes them off the launch), so a CTA that finishes early takes more work
+// instead of waiting on a fixed share, and no memory holds the queue: launches in flight
+// together, replayed graphs among them, share nothing.  A work item is two 128-row query tiles (A: rows 256*qb .. +127,
 // B: the next 128) of one (batch, query head); both tiles share every K/V tile
 // loaded for the item.  Warp roles (12 warps, three warpgroups):
 //   warps 0-3  softmax of tile A, warps 4-7 softmax of tile B: thread i of a
 //              group owns query row i, which is TMEM lane i of its S and O;
-//   warps 8,10 TMA producers: warp 8 loads Q_A and Q_B per item (the next
-//              item's Q is prefetched into L2 early) and the K tiles, warp 10
+//   warps 8,10 TMA producers: warp 8 asks for the items, loads Q_A and Q_B of each
+//              (the next one's are prefetched into L2) and the K tiles, warp 10
 //              the V tiles, each through its own ring (2 stages at d = 128, 4
 //              at d = 64) that runs on across items; K is released after the
 //              second S MMA reading it, V after the second PV;
@@ -68,20 +69,10 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
-#include <atomic>
-#include <mutex>
-
 #include "internal.h"
 #include "ptx.cuh"
 
 namespace kvattn {
-
-// Work-queue counters of the prefill kernel: slot i holds (next ticket, CTAs
-// done) of one launch; launches take slots in turn, and each launch's last CTA
-// zeroes its slot, so launches in flight at the same time (up to kQueueSlots)
-// never share counters.  Zero at load time.
-constexpr int kQueueSlots = 1024;
-__device__ unsigned g_prefill_queue[2 * kQueueSlots];
 
 namespace {
 
@@ -111,7 +102,7 @@ struct PrefillCfg {
   static constexpr int kKOff = kQOff + 2 * kTileBytes;          // K stages 0..kKStages-1
   static constexpr int kVOff = kKOff + kKStages * kTileBytes;   // V stages 0..kVStages-1
   static constexpr int kBarOff = kVOff + kVStages * kTileBytes;
-  static constexpr int kOrderOff = kBarOff + 256;        // cached forms: sequences by length, longest first
+  static constexpr int kOrderOff = kBarOff + 320;        // cached forms: sequences by length, longest first
   static constexpr int kMaxOrdered = 256;
   static constexpr int kUsed = kOrderOff + kMaxOrdered * 4;
   // one CTA per SM: it owns all 512 TMEM columns
@@ -137,9 +128,11 @@ enum Bar {
   B_ODONE = B_PFULL + 2,            // +tile: last PV of an item done
   B_OFREE = B_ODONE + 2,            // +tile: the softmax group has read O out
   B_DRAIN = B_OFREE + 2,            // only used when a bounded wait gave up
-  B_COUNT = B_DRAIN + 1
+  B_NEXT = B_DRAIN + 1,             // the answer to the request for a further item
+  B_COUNT = B_NEXT + 1
 };
-static_assert(B_COUNT * 8 + 8 + 4 * kItemSlots <= 256, "barrier block");
+constexpr int kNextOff = (B_COUNT * 8 + 8 + 4 * kItemSlots + 15) / 16 * 16;   // that answer, in the barrier block
+static_assert(kNextOff + 16 <= 320, "barrier block");
 
 // Where K and V come from.
 // KV_DENSE_GROUPED: the dense form with its items in the cached forms' order.
@@ -148,17 +141,20 @@ enum KvSource { KV_DENSE = 0, KV_CACHE = 1, KV_PAGED = 2, KV_DENSE_GROUPED = 3 }
 // Register split (setmaxnreg): 384 threads launch with 168 registers each; the producer
 // warpgroup (two TMA warps, the MMA warp and one more) gives back down to regs_io() so
 // each softmax thread can hold its 128 scores and the exponential temporaries.  Chosen
-// per form by ptxas's spill report: the dense d = 128 softmax needs 216 registers, the
-// other forms spill less with 208 and 88 for the producers (the cached forms' producers
-// also track the sequence lengths and page-table entries).
+// per form by ptxas's spill report and the clock: the ungrouped dense softmax needs 216
+// (d = 64: 208) registers; the other forms' producers, which also find items, lengths and
+// blocks, spilled at 88 (cached chunks 376 us instead of 366 at 104; windowed prompts of
+// 32 / 8 heads 178 at 88, 174 at 104, 170 at 120).
+template <int KV, bool WIN>
+constexpr bool kManyIoRegs = WIN && KV == KV_DENSE_GROUPED;
 template <int D, int KV, bool WIN = false>
-constexpr int regs_softmax() { return D == 128 && KV == KV_DENSE && !WIN ? 216 : 208; }
+constexpr int regs_softmax() { return KV == KV_DENSE ? (D == 128 ? 216 : 208) : (kManyIoRegs<KV, WIN> ? 192 : 200); }
 template <int D, int KV, bool WIN = false>
-constexpr int regs_io() { return D == 128 && KV == KV_DENSE && !WIN ? 72 : 88; }
-static_assert(2 * 128 * regs_softmax<128, KV_DENSE>() + 128 * regs_io<128, KV_DENSE>() <= 168 * kThreads,
-              "register split exceeds the launch");
-static_assert(2 * 128 * regs_softmax<64, KV_PAGED>() + 128 * regs_io<64, KV_PAGED>() <= 168 * kThreads,
-              "register split exceeds the launch");
+constexpr int regs_io() { return KV == KV_DENSE ? (D == 128 ? 72 : 88) : (kManyIoRegs<KV, WIN> ? 120 : 104); }
+template <int D, int KV, bool WIN = false>
+constexpr bool kSplitFits = 2 * 128 * regs_softmax<D, KV, WIN>() + 128 * regs_io<D, KV, WIN>() <= 168 * kThreads;
+static_assert(kSplitFits<128, KV_DENSE> && kSplitFits<64, KV_DENSE> && kSplitFits<128, KV_PAGED> &&
+              kSplitFits<128, KV_DENSE_GROUPED, true>, "register split exceeds the launch");
 template <int KV>
 constexpr bool kDenseKv = KV == KV_DENSE || KV == KV_DENSE_GROUPED;
 
@@ -173,9 +169,7 @@ struct PrefillParams {
   void* o;
   float* lse;
   unsigned* status;
-  unsigned* next_item;   // work queue: tickets handed out after the first gridDim.x items
-  unsigned* done_ctas;   // the last CTA to finish resets both counters for the next launch
-  int B, N, Hq, Hkv, G, n_qblocks, n_ktiles, n_items;   // N: queries per sequence (Nq)
+  int B, N, Hq, Hkv, G, n_qblocks, n_ktiles;   // N: queries per sequence (Nq)
   float scale_log2;
   int causal, o_bf16;
   // cached forms only
@@ -393,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars[B_OFREE + s], 4);
     }
     mbar_init(&bars[B_DRAIN], 1);
+    mbar_init(&bars[B_NEXT], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -430,14 +425,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < kMaxStages; ++i) last[i] = -1;
     bool ok = true, clean_end = false;
-    for (int w = blockIdx.x;; ++it) {
+    void* const answer = reinterpret_cast<uint8_t*>(bars) + kNextOff;
+    int w = blockIdx.x;                           // the item, or -1: no more work
+    constexpr int kAsked = -2;                    // K producer: the next item has been asked for
+    for (;; ++it) {
       Item itm;
-      int w_next = 0;
       if (is_k) {
         // Q of the previous item no longer read (this also means its copy landed), and
         // that item read by every softmax warp and by the V producer
         if (it > 0 && !wait_or_abort(&bars[B_QEMPTY], (it - 1) & 1, abort_flag, p.status)) break;
-        if (w >= p.n_items) {
+        if (w < 0) {
           // no more work: complete B_QFULL phase `it` without a copy
           if (lane == 0) {
             item_slot[it % kItemSlots] = -1;
@@ -446,10 +443,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           clean_end = true;
           break;
         }
-        if (lane == 0) item_slot[it % kItemSlots] = w;
+        if (lane == 0) {
+          item_slot[it % kItemSlots] = w;
+          take_pending_cta(answer, &bars[B_NEXT]);
+        }
         itm = item_of<KV, WIN>(w, p, order);
-        if (lane == 0) w_next = (int)gridDim.x + (int)atomicAdd(p.next_item, 1u);
-        w_next = __shfl_sync(0xffffffffu, w_next, 0);
+        w = kAsked;
         ++q_loaded;
         if (lane == 0) {
           mbar_arrive_expect_tx(&bars[B_QFULL], 2 * C::kTileBytes);
@@ -459,14 +458,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int hh = 0; hh < C::kHalves; ++hh)
               tma_load_4d(smem + C::kQOff + t * C::kTileBytes + hh * C::kHalfBytes, &tmQ, &bars[B_QFULL], hh * 64,
                           itm.h, ((WIN ? p.item_tiles : 2) * itm.qb + t) * kBM, itm.b, once);
-          if (w_next < p.n_items) {                 // warm L2 with the next item's Q
-            const Item nx = item_of<KV, WIN>(w_next, p, order);
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int hh = 0; hh < C::kHalves; ++hh)
-                tma_prefetch_4d(&tmQ, hh * 64, nx.h, (2 * nx.qb + t) * kBM, nx.b);
-          }
         }
       } else {
         // the item the K producer published (the V copies of an item follow its Q copies)
@@ -537,7 +528,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      w = w_next;
+      if (is_k) {
+        // the next item, asked for when this one began
+        if (!wait_or_abort(&bars[B_NEXT], it & 1, abort_flag, p.status)) break;
+        w = __shfl_sync(0xffffffffu, lane == 0 ? taken_cta(answer) : 0, 0);
+        if (w >= 0 && lane == 0) {                  // warm L2 with its Q
+          const Item nx = item_of<KV, WIN>(w, p, order);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int hh = 0; hh < C::kHalves; ++hh)
+              tma_prefetch_4d(&tmQ, hh * 64, nx.h, (2 * nx.qb + t) * kBM, nx.b);
+        }
+      }
+    }
+    // a wait gave up: the items not started are dropped, so that the launch ends soon (each of
+    // their CTAs might run out of its wait, too), and no answer may land after the CTA's end
+    if (is_k && !clean_end && lane == 0) {
+      int phase = w == kAsked ? it : q_loaded;
+      while (w != -1) {
+        if (w != kAsked) take_pending_cta(answer, &bars[B_NEXT]);
+        if (!mbar_wait(&bars[B_NEXT], (phase++) & 1)) break;
+        w = taken_cta(answer);
+      }
     }
     // no copy may still be landing in shared memory when the CTA exits (after a clean
     // end, the wait on B_QEMPTY above already covered the last Q copy)
@@ -922,31 +935,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
-  if (threadIdx.x == 0 && atomicAdd(p.done_ctas, 1u) == gridDim.x - 1) {
-    // every CTA has taken its last ticket: leave the queue at zero for the next launch
-    atomicExch(p.next_item, 0u);
-    atomicExch(p.done_ctas, 0u);
-  }
-}
-
-// This launch's pair of queue counters on the current device.
-cudaError_t queue_slot(unsigned** next, unsigned** done) {
-  constexpr int kMaxDevices = 64;
-  static void* base[kMaxDevices] = {};
-  static std::atomic<unsigned> launches[kMaxDevices];
-  static std::mutex mu;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  {
-    std::lock_guard<std::mutex> g(mu);
-    if (!base[dev] && (e = cudaGetSymbolAddress(&base[dev], g_prefill_queue)) != cudaSuccess) return e;
-  }
-  const unsigned slot = launches[dev].fetch_add(1u) % kQueueSlots;
-  *next = static_cast<unsigned*>(base[dev]) + slot;
-  *done = static_cast<unsigned*>(base[dev]) + kQueueSlots + slot;
-  return cudaSuccess;
 }
 
 template <int D, int KV, bool WIN = false>
@@ -992,7 +980,6 @@ cudaError_t run_prefill(const PrefillLaunch& a, cudaStream_t stream) {
   p.n_ktiles = (a.N + kBN - 1) / kBN;
   const long long items = (long long)p.n_qblocks * a.Hq * a.B;
   if (items > INT32_MAX) return cudaErrorInvalidValue;
-  p.n_items = (int)items;
   p.scale_log2 = a.scale * kLog2e;
   p.causal = a.causal;
   p.o_bf16 = a.o_bf16;
@@ -1004,8 +991,6 @@ cudaError_t run_prefill(const PrefillLaunch& a, cudaStream_t stream) {
   p.sinks = a.sinks;
   p.max_keys = KV == KV_PAGED ? a.max_blocks * kPageTokens : (KV == KV_CACHE ? a.capacity : a.N);
   if (!kDenseKv<KV> && a.max_seqlen > 0 && a.max_seqlen < p.max_keys) p.max_keys = a.max_seqlen;
-  cudaError_t qe = queue_slot(&p.next_item, &p.done_ctas);
-  if (qe != cudaSuccess) return qe;
   auto kern = prefill_kernel<D, KV, WIN>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -1016,11 +1001,8 @@ cudaError_t run_prefill(const PrefillLaunch& a, cudaStream_t stream) {
   if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
   if (fa.numRegs * kThreads < 2 * 128 * regs_softmax<D, KV, WIN>() + 128 * regs_io<D, KV, WIN>())
     return cudaErrorInvalidConfiguration;
-  // persistent: one CTA per SM (each owns all 512 TMEM columns)
-  int dev = 0, sms = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  const int grid = p.n_items < sms ? p.n_items : sms;
+  // one CTA per SM runs at a time (each owns all 512 TMEM columns)
+  const unsigned grid = (unsigned)items;
   if constexpr (WIN) return launch_beside(kern, dim3(grid), kThreads, C::kSmemBytes, stream, true, tq, tk, tv, p);
   kern<<<grid, kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();

@@ -136,6 +136,34 @@ __device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, 
                : "memory");
 }
 
+// ---------------------------------------------------------------- cluster launch control
+// Take a CTA of this grid that has not started yet off the launch: its block index, or that
+// none is left, arrives in `response` (16 bytes, 16-byte aligned, shared memory) and completes
+// 16 bytes on `bar`.  After "none left" no further request may be made.
+__device__ __forceinline__ void take_pending_cta(void* response, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(response)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+
+// blockIdx.x of the CTA taken, or -1; `response` may then be written again.
+__device__ __forceinline__ int taken_cta(const void* response) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 r, [%1];\n\t"
+      "mov.s32 %0, -1;\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+      : "=&r"(x)
+      : "r"(smem_u32(response))
+      : "memory");
+  fence_proxy_async_smem();   // the next response is written by the async proxy
+  return x;
+}
+
 // ---------------------------------------------------------------- warp MMA
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"

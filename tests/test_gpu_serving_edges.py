@@ -73,3 +73,67 @@ def test_an_angle_table_made_on_another_stream():
     side.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------------- graphs beside eager calls
+@pytest.mark.parametrize("cached", [False, True])
+@pytest.mark.parametrize("windowed", [False, True])
+def test_a_captured_prefill_runs_beside_eager_ones(windowed, cached):
+    """A captured prefill replays on one stream while far more eager ones than a library could keep queues
+    for run on another: no launch's items are another's."""
+    Hq, Hkv, d = 16, 2, 64
+
+    def case(B, N, seed):
+        q, k, v = synth.prefill_inputs(B, Hq, Hkv, N, d, seed=seed, device="cuda")
+        n = to_dev_i32([N] * B)
+        mask = (70, 4) if windowed else ()
+
+        def go(o):
+            if cached:
+                fn = kv.attn_prefill_cache_window if windowed else kv.attn_prefill_cache
+                fn(q, k, v, n, o, *mask)
+            else:
+                fn = kv.attn_prefill_window if windowed else kv.attn_prefill
+                fn(q, k, v, o, *mask)
+        want = torch.full_like(q, float("nan"), dtype=torch.float32)
+        go(want)
+        return go, want
+
+    long, short = case(4, 2000, 1), case(1, 300, 2)     # 512 items, and 32
+    o = torch.empty_like(long[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        long[0](o)
+    outs = [torch.empty_like(short[1]) for _ in range(8)]
+    side = torch.cuda.Stream()
+    for round_ in range(3):
+        o.fill_(float("nan"))
+        for x in outs:
+            x.fill_(float("nan"))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                g.replay()
+        for i in range(1100):
+            short[0](outs[i % 8])
+        torch.cuda.synchronize()
+        assert torch.equal(o, long[1])
+        assert all(torch.equal(x, short[1]) for x in outs)
+
+
+@pytest.mark.parametrize("windowed", [False, True])
+def test_prefills_of_many_items_on_several_streams(windowed):
+    """Four launches of more items than SMs at once: each output is whole."""
+    q, k, v = synth.prefill_inputs(3, 20, 4, 1200, 128, seed=5, device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    mask = (300, 4) if windowed else ()
+    fn = kv.attn_prefill_window if windowed else kv.attn_prefill
+    want = torch.empty_like(q, dtype=torch.float32)
+    fn(q, k, v, want, *mask)
+    outs = [torch.full_like(want, float("nan")) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, o in zip(streams, outs):
+            fn(q, k, v, o, *mask, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
