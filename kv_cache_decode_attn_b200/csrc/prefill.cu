@@ -761,6 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (c + e < p.sinks) mx = fmaxf(mx, __uint_as_float(r[e]));
           }
           m = mx * p.scale_log2;
+          const float neg_mu = (m == -INFINITY) ? 0.f : -m;   // every first token at -inf: p = 0
 #pragma unroll 1
           for (int c = 0; c < itm.cols; c += 16) {   // P of these columns lies below S of the next
             uint32_t r[16], pk[8];
@@ -768,8 +769,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              const float p0 = c + e < p.sinks ? ex2(fmaf(__uint_as_float(r[e]), p.scale_log2, -m)) : 0.f;
-              const float p1 = c + e + 1 < p.sinks ? ex2(fmaf(__uint_as_float(r[e + 1]), p.scale_log2, -m)) : 0.f;
+              const float p0 = c + e < p.sinks ? ex2(fmaf(__uint_as_float(r[e]), p.scale_log2, neg_mu)) : 0.f;
+              const float p1 = c + e + 1 < p.sinks ? ex2(fmaf(__uint_as_float(r[e + 1]), p.scale_log2, neg_mu)) : 0.f;
               l += p0 + p1;
               pk[e / 2] = pack_bf16x2(p0, p1);
             }

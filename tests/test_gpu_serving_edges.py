@@ -1,14 +1,17 @@
 """GPU tests of what the calls do at the edges of their arguments and of how they are used."""
 
+import numpy as np
 import pytest
 import torch
 
 import synth
+from oracle import serving
 
 pytestmark = pytest.mark.gpu
 
 kv = pytest.importorskip("kv_cache_decode_attn_b200")
-from tests.gpu_util import to_dev_i32  # noqa: E402
+from tests.gpu_util import f64, to_dev_i32  # noqa: E402
+from tests.test_gpu_window import check, host_cache  # noqa: E402
 
 
 @pytest.fixture(autouse=True)
@@ -137,3 +140,54 @@ def test_prefills_of_many_items_on_several_streams(windowed):
             fn(q, k, v, o, *mask, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+# ---------------------------------------------------------------- first tokens whose scores are -inf
+def overflowing(q, k, sinks):
+    """Value 0 of every head: its product with a first token's overflows fp32 to -inf, with any other key's is 0."""
+    q[..., 0] = 1e20
+    k[..., 0] = 0.0
+    k[:, :sinks, :, 0] = -1e20
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sinks", [1, 4, 16, 50, 64, 100])
+@pytest.mark.parametrize("N,Hq,B", [(700, 4, 2), (900, 24, 2)])      # one and two query tiles per item
+def test_first_tokens_with_infinite_scores_drop_out(d, sinks, N, Hq, B):
+    """A first token at -inf weighs nothing, whichever tile holds it.  Rows that see nothing else have no
+    finite score and are left out."""
+    window, Hkv = 90, 2
+    q, k, v = synth.prefill_inputs(B, Hq, Hkv, N, d, seed=sinks + d, device="cuda")
+    overflowing(q, k, sinks)
+    o = torch.full((B, N, Hq, d), float("nan"), device="cuda")
+    lse = torch.full((B, Hq, N), float("nan"), device="cuda")
+    kv.attn_prefill_window(q, k, v, o, window, sinks, lse=lse)
+    args = f64(q), f64(k)
+    ref = serving.attention_window(*args, f64(v), d ** -0.5, [N] * B, window, sinks)
+    weight = serving.attention_window(*args, np.abs(f64(v)), d ** -0.5, [N] * B, window, sinks)[0]
+    check(o[:, sinks:], lse[:, :, sinks:], (ref[0][:, sinks:], ref[1][:, :, sinks:]), weight[:, sinks:])
+
+
+@pytest.mark.parametrize("T", [1, 8, 300])
+@pytest.mark.parametrize("paged", [False, True])
+def test_cached_first_tokens_with_infinite_scores_drop_out(T, paged):
+    """The same over a cache: every decode form, and the chunk's."""
+    Hq, Hkv, d, window, sinks, lens = 16, 2, 128, 100, 4, [700 + T, 1500 + T]
+    case = synth.decode_inputs(2, T, Hq, Hkv, d, 0, 0, seed=T, device="cuda", paged=paged, lengths=[L - T for L in lens])
+    case.q[..., 0] = 1e20
+    kc, vc = (case.k_pool, case.v_pool) if paged else (case.k_cache, case.v_cache)
+    kc[..., 0] = 0.0
+    for b in range(2):
+        if paged:
+            kc[int(case.page_table[b, 0]), :sinks, :, 0] = -1e20
+        else:
+            kc[b, :sinks, :, 0] = -1e20
+    host, q = host_cache(case, lens), f64(case.q)
+    ref = serving.attention_window(q, *host, d ** -0.5, lens, window, sinks)
+    weight = serving.attention_window(q, host[0], np.abs(host[1]), d ** -0.5, lens, window, sinks)[0]
+    table = to_dev_i32(case.page_table) if paged else None
+    for call in (kv.attn_decode_window, kv.attn_prefill_cache_window):
+        o = torch.full((2, T, Hq, d), float("nan"), device="cuda")
+        lse = torch.full((2, Hq, T), float("nan"), device="cuda")
+        call(case.q, kc, vc, to_dev_i32(lens), o, window, sinks, lse=lse, page_table=table)
+        check(o, lse, ref, weight)
