@@ -43,7 +43,6 @@ namespace kvattn {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D, int MT, bool FP8>
 struct DecodeCfg {
@@ -551,7 +550,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
         }
         const float inv = lsum > 0.f ? (FP8 ? v_scale / lsum : 1.f / lsum) : 0.f;
         const float4 out = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        const float lse = bad ? NAN : (lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY);
+        const float lse = bad ? NAN : row_lse(mrow, lsum);
         if (p.out.on) {
           p.out.store4<D>(b, g, r, 4 * v, out);
           if (v == 0) p.out.store_lse(b, g, r, lse);
@@ -638,7 +637,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, MT, FP8>::kThreads, DecodeCfg<D, 
     const float inv = lsum > 0.f ? (FP8 ? v_scale / lsum : 1.f / lsum) : 0.f;
     *reinterpret_cast<float4*>(out + (size_t)r * D + col) =
         make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (col == 0) p.part_lse[item * p.R + r] = lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY;
+    if (col == 0) p.part_lse[item * p.R + r] = row_lse(mrow, lsum);
   }
   break;
   }
@@ -790,7 +789,7 @@ __global__ void __launch_bounds__(256, kBatch >= 8 ? 2 : 5) decode_combine_kerne
     for (int c = 32 + lane; c < nc; c += 32) {
       const float lc = __ldg(chunk_lse(c));
       if (lc == -INFINITY) continue;
-      if (lc > m) {
+      if (!(lc <= m)) {   // NaN too: it stays, whatever m is
         sum = sum * expf(m - lc) + 1.f;
         m = lc;
       } else {

@@ -32,7 +32,6 @@
 namespace kvattn {
 namespace {
 
-constexpr float kLn2 = 0.6931471805599453f;
 
 struct Fp8StCfg {
   static constexpr int kConsumerWarps = 4;
@@ -307,7 +306,7 @@ __global__ void __launch_bounds__(Fp8StCfg::kThreads, 3)
     const float inv = lsum > 0.f ? vs / lsum : 0.f;
     *reinterpret_cast<float4*>(out + (size_t)r * 128 + col) =
         make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (col == 0) p.part_lse[item * p.R + r] = lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY;
+    if (col == 0) p.part_lse[item * p.R + r] = row_lse(mrow, lsum);
   }
 }
 

@@ -33,8 +33,6 @@
 namespace kvattn {
 namespace {
 
-constexpr float kLn2 = 0.6931471805599453f;
-
 template <int D, bool FP8>
 struct Rows8Cfg {
   static_assert(!FP8 || D == 128, "FP8 caches are built for d = 128");
@@ -444,7 +442,7 @@ __global__ void __launch_bounds__(Rows8Cfg<D, FP8>::kThreads, Rows8Cfg<D, FP8>::
         }
         const float inv = lsum > 0.f ? (FP8 ? v_scale / lsum : 1.f / lsum) : 0.f;
         const float4 out = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        const float lse = bad ? NAN : (lsum > 0.f ? (mrow + log2f(lsum)) * kLn2 : -INFINITY);
+        const float lse = bad ? NAN : row_lse(mrow, lsum);
         if (p.out.on) {   // sg is still this segment
           p.out.store4<D>(sg.b, sg.g, r, 4 * v, bad ? make_float4(NAN, NAN, NAN, NAN) : out);
           if (v == 0) p.out.store_lse(sg.b, sg.g, r, lse);

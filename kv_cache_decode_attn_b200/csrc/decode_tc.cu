@@ -48,7 +48,6 @@ namespace {
 constexpr int kRows = 128;   // MMA M (query rows per KV head, padded)
 constexpr int kTok = kDecodeTcTile;   // keys per K/V tile (the host's tensor-map box)
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int kStages = 2;    // K/V ring stages (S is double-buffered in TMEM)
 constexpr int kCtasPerSm = kDecodeTcCtasPerSm;   // shared memory and TMEM of one CTA
@@ -798,7 +797,7 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
                             __uint_as_float(r[e + 2]) * inv_l, __uint_as_float(r[e + 3]) * inv_l);
         }
       }
-      const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      const float lse = row_lse(m, l);
       if (SEL && live && p.out.on) p.out.store_lse(b, g, t0 * p.G + row, lse);
       else if (live) p.part_lse[row0 + row] = lse;
     } else if (SEL && live && p.out.on) {

@@ -57,6 +57,12 @@ inline DirectOut direct_out(const DecodeLaunch& a) {
   return d;
 }
 
+// Log-sum-exp of a row from its reference maximum m (base 2, scale folded in) and the sum l
+// of 2^(score - m): -inf where every key weighs nothing, NaN where a score is NaN.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 struct SplitParams {
   const __nv_bfloat16* q;
   const float* k_scale;   // FP8 caches: per-KV-head scales (else unused)

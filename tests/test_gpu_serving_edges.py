@@ -191,3 +191,55 @@ def test_cached_first_tokens_with_infinite_scores_drop_out(T, paged):
         lse = torch.full((2, Hq, T), float("nan"), device="cuda")
         call(case.q, kc, vc, to_dev_i32(lens), o, window, sinks, lse=lse, page_table=table)
         check(o, lse, ref, weight)
+
+
+# ------------------------------------------------------------------------------- NaN scores
+@pytest.mark.parametrize("num_splits", [0, 1, 7])
+@pytest.mark.parametrize("windowed", [False, True])
+@pytest.mark.parametrize("kind,T,Hq,Hkv,d", [("contig", 1, 8, 1, 128), ("paged", 1, 4, 2, 64), ("paged", 2, 16, 2, 128),
+                                             ("contig", 8, 8, 2, 128), ("fp8", 1, 8, 1, 128), ("fp8", 2, 12, 1, 128),
+                                             ("fp8", 4, 8, 1, 128), ("fp8", 33, 8, 1, 128)])
+def test_a_row_with_nan_scores_is_nan_in_both_outputs(kind, T, Hq, Hkv, d, windowed, num_splits):
+    """NaN in one query row: that row's output and LSE are NaN, not an LSE of -inf (a row without keys);
+    the other rows are exact."""
+    lens = [T + 40, T + 1900]
+    case = synth.decode_inputs(2, T, Hq, Hkv, d, 0, 0, seed=T, device="cuda", paged=kind != "contig",
+                               lengths=[L - T for L in lens], fp8=kind == "fp8")
+    host, q = host_cache(case, lens), f64(case.q)
+    window, sinks = (300, 5) if windowed else (1 << 30, 0)
+    ref = serving.attention_window(q, *host, d ** -0.5, lens, window, sinks)
+    weight = serving.attention_window(q, host[0], np.abs(host[1]), d ** -0.5, lens, window, sinks)[0]
+    case.q[1, T - 1, Hq - 1, 3] = float("nan")
+    table = to_dev_i32(case.page_table) if case.paged else None
+    kc, vc = (case.k_pool, case.v_pool) if case.paged else (case.k_cache, case.v_cache)
+    scales = [torch.as_tensor(s, device="cuda") for s in (case.k_scale, case.v_scale)] if case.fp8 else []
+    o = torch.zeros(2, T, Hq, d, device="cuda")
+    lse = torch.zeros(2, Hq, T, device="cuda")
+    kw = dict(lse=lse, page_table=table, num_splits=num_splits)
+    if windowed:
+        fn = kv.attn_decode_window_fp8 if case.fp8 else kv.attn_decode_window
+        fn(case.q, kc, vc, *scales, to_dev_i32(lens), o, window, sinks, **kw)
+    else:
+        fn = kv.attn_decode_fp8 if case.fp8 else kv.attn_decode
+        fn(case.q, kc, vc, *scales, to_dev_i32(lens), o, **kw)
+    assert torch.isnan(o[1, T - 1, Hq - 1]).all()
+    assert torch.isnan(lse[1, Hq - 1, T - 1])
+    o[1, T - 1, Hq - 1] = torch.as_tensor(ref[0][1, T - 1, Hq - 1])
+    lse[1, Hq - 1, T - 1] = float(ref[1][1, Hq - 1, T - 1])
+    check(o, lse, ref, weight)
+
+
+@pytest.mark.parametrize("splits", [34, 70])
+@pytest.mark.parametrize("T,d", [(1, 128), (1, 64), (8, 128)])
+def test_nan_in_a_late_chunk_behind_an_empty_one(splits, T, d):
+    """More than 32 chunks, the first 32 with scores of -inf and one after them with a NaN key: the merged
+    LSE is NaN as the output is."""
+    L = 64 * splits
+    case = synth.decode_inputs(1, T, 8, 2, d, 0, 0, seed=4, device="cuda", lengths=[L - T])
+    case.q[..., 0] = 1e20
+    case.k_cache[..., 0] = 0.0
+    case.k_cache[0, :32 * 64, :, 0] = -1e20
+    case.k_cache[0, 32 * 64 + 5] = float("nan")
+    o, lse = torch.zeros(1, T, 8, d, device="cuda"), torch.zeros(1, 8, T, device="cuda")
+    kv.attn_decode(case.q, case.k_cache, case.v_cache, to_dev_i32([L]), o, lse, num_splits=splits)
+    assert torch.isnan(o).all() and torch.isnan(lse).all()
