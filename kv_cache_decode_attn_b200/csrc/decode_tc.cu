@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(tc_threads<FP8>(), kCtasPerSm)
   const int L = sk.L;
   // invalid lengths: their rows are made NaN by the combine kernel
   if (sk.bad) {
-    if (SEL && threadIdx.x == 0) atomicOr(p.status, DEV_SEQLEN);
+    if (threadIdx.x == 0) atomicOr(p.status, DEV_SEQLEN);
     if (SEL && p.out.on) {
       const int r0 = rt * p.TT * p.G;
       p.out.store_nan<D>(b, g, r0, min(r0 + p.TT * p.G, p.R), threadIdx.x, blockDim.x);

@@ -243,3 +243,37 @@ def test_nan_in_a_late_chunk_behind_an_empty_one(splits, T, d):
     o, lse = torch.zeros(1, T, 8, d, device="cuda"), torch.zeros(1, 8, T, device="cuda")
     kv.attn_decode(case.q, case.k_cache, case.v_cache, to_dev_i32([L]), o, lse, num_splits=splits)
     assert torch.isnan(o).all() and torch.isnan(lse).all()
+
+
+# ---------------------------------------------------------------------- invalid lengths, every form
+@pytest.mark.parametrize("via", ["plain", "wide window", "no prefix"])
+@pytest.mark.parametrize("num_splits", [0, 3])
+@pytest.mark.parametrize("kind,T,Hq,Hkv", [("contig", 8, 16, 2), ("paged", 8, 16, 2), ("paged", 40, 16, 2), ("fp8", 8, 16, 2),
+                                           ("paged", 1, 16, 2), ("fp8", 1, 16, 2)])
+def test_invalid_lengths_are_flagged_by_plain_decode_too(kind, T, Hq, Hkv, num_splits, via):
+    """What attn_decode states, on the tensor-core kernel as on the others, and through the calls that end in
+    it: a window that hides nothing, a shared prefix of no blocks."""
+    if via == "no prefix" and kind == "contig":
+        pytest.skip("sharing needs pages")
+    lens = [T + 50, T + 300]
+    case = synth.decode_inputs(2, T, Hq, Hkv, 128, 0, 0, seed=T, device="cuda", paged=kind != "contig",
+                               lengths=[L - T for L in lens], fp8=kind == "fp8")
+    table = to_dev_i32(case.page_table) if case.paged else None
+    kc, vc = (case.k_pool, case.v_pool) if case.paged else (case.k_cache, case.v_cache)
+    scales = [torch.as_tensor(s, device="cuda") for s in (case.k_scale, case.v_scale)] if case.fp8 else []
+    for wrong in ([T - 1, lens[1]], [lens[0], max(lens) + 1]):
+        o, lse = torch.zeros(2, T, Hq, 128, device="cuda"), torch.zeros(2, Hq, T, device="cuda")
+        n, kw = to_dev_i32(wrong), dict(lse=lse, max_seqlen_k=max(lens), num_splits=num_splits)
+        bad = 0 if wrong[0] < T else 1
+        if via == "plain":
+            fn = kv.attn_decode_fp8 if case.fp8 else kv.attn_decode
+            fn(case.q, kc, vc, *scales, n, o, page_table=table, **kw)
+        elif via == "wide window":
+            fn = kv.attn_decode_window_fp8 if case.fp8 else kv.attn_decode_window
+            fn(case.q, kc, vc, *scales, n, o, 1 << 20, 0, page_table=table, **kw)
+        else:
+            fn = kv.attn_decode_shared_fp8 if case.fp8 else kv.attn_decode_shared
+            fn(case.q, kc, vc, *scales, n, table, table[0, :0], o, **kw)
+        assert kv.attn_get_device_status(clear=True) == kv.ATTN_DEV_SEQLEN
+        assert torch.isnan(o[bad]).all() and torch.isnan(lse[bad]).all()
+        assert torch.isfinite(o[1 - bad]).all() and torch.isfinite(lse[1 - bad]).all()
