@@ -431,8 +431,8 @@ def attn_decode_window_fp8(q, k_cache, v_cache, k_scale, v_scale, seqlens_k, o, 
             workspace = decode_window_workspace(*q.shape[:3], k_cache.shape[2], q.shape[3],
                                                 _longest(k_cache, page_table, max_seqlen_k), window, sinks, num_splits,
                                                 q.device)
-    st = _marshal.decode_window(*here, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, o, window, sinks, lse,
-                                page_table, max_seqlen_k, scale, num_splits, workspace)
+    st = _marshal.decode_window_fp8(*here, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, o, window, sinks, lse,
+                                    page_table, max_seqlen_k, scale, num_splits, workspace)
     _check("attn_decode_window_fp8", st)
 
 
@@ -450,7 +450,7 @@ def decode_shared_workspace(B, T, Hq, Hkv, d, max_seqlen_k, prefix_blocks, num_s
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _decode_shared(name, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_table, prefix_table, o, lse,
+def _decode_shared(name, marshal, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_table, prefix_table, o, lse,
                    max_seqlen_k, scale, causal, num_splits, workspace, stream) -> None:
     here = _here(q, stream)
     if workspace is None:
@@ -460,8 +460,8 @@ def _decode_shared(name, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_
             workspace = decode_shared_workspace(*q.shape[:3], k_cache.shape[2], q.shape[3],
                                                 _longest(k_cache, page_table, max_seqlen_k), prefix_table.shape[0],
                                                 num_splits, q.device)
-    st = _marshal.decode_shared(*here, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_table, prefix_table, o,
-                                lse, max_seqlen_k, scale, causal, num_splits, workspace)
+    st = marshal(*here, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_table, prefix_table, o, lse,
+                 max_seqlen_k, scale, causal, num_splits, workspace)
     _check(name, st)
 
 
@@ -471,16 +471,17 @@ def attn_decode_shared(q, k_cache, v_cache, seqlens_k, page_table, prefix_table,
     first blocks: prefix_table int32 ``[prefix_blocks]`` names them (``page_table[0, :n]`` serves)
     and page_table's first prefix_blocks columns are not read.  The prefix is read once for the
     whole batch, or by each sequence where that is faster (few sequences, a short prefix).  seqlens_k counts the prefix and the T new tokens."""
-    _decode_shared("attn_decode_shared", q, k_cache, v_cache, None, None, seqlens_k, page_table, prefix_table, o, lse,
-                   max_seqlen_k, scale, causal, num_splits, workspace, stream)
+    _decode_shared("attn_decode_shared", _marshal.decode_shared, q, k_cache, v_cache, None, None, seqlens_k, page_table,
+                   prefix_table, o, lse, max_seqlen_k, scale, causal, num_splits, workspace, stream)
 
 
 def attn_decode_shared_fp8(q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_table, prefix_table, o, lse=None,
                            max_seqlen_k=0, scale=None, causal=True, num_splits=0, workspace=None,
                            stream=None) -> None:
     """``attn_decode_shared`` over an FP8 cache (scales as ``attn_decode_fp8``)."""
-    _decode_shared("attn_decode_shared_fp8", q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_table,
-                   prefix_table, o, lse, max_seqlen_k, scale, causal, num_splits, workspace, stream)
+    _decode_shared("attn_decode_shared_fp8", _marshal.decode_shared_fp8, q, k_cache, v_cache, k_scale, v_scale,
+                   seqlens_k, page_table, prefix_table, o, lse, max_seqlen_k, scale, causal, num_splits, workspace,
+                   stream)
 
 
 # ------------------------------------------------- norm, rotation and append in one pass
@@ -526,8 +527,8 @@ def kv_append_norm_rope_fp8(k_cache, v_cache, q, k_new, v_new, q_out, k_scale, v
                             page_table=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
                             stream=None) -> None:
     """``kv_append_norm_rope`` into an FP8 cache (quantised as ``kv_append_fp8`` does)."""
-    st = _marshal.append_norm_rope(*_here(q, stream), k_cache, v_cache, q, k_new, v_new, q_out, k_scale, v_scale,
-                                   rope, cache_lens, page_table, q_weight, k_weight, eps, interleaved)
+    st = _marshal.append_norm_rope_fp8(*_here(q, stream), k_cache, v_cache, q, k_new, v_new, q_out, k_scale, v_scale,
+                                       rope, cache_lens, page_table, q_weight, k_weight, eps, interleaved)
     _check("kv_append_norm_rope_fp8", st)
 
 

@@ -117,29 +117,27 @@ struct Queries {
 };
 
 // The cache of B sequences: contiguous [B, capacity, Hkv, d], or pools [num_blocks, 16, Hkv, d] with a
-// page table [B, max_blocks]; lengths [B]; FP8: scales [Hkv].
+// page table [B, max_blocks]; lengths [B]; FP8 (the call's say, not the arguments'): scales [Hkv].
 struct Cache {
   int max_blocks = 0, num_blocks = 0, capacity = 0, Hkv;
-  bool fp8;
   void *k, *v;
   float *k_scale = nullptr, *v_scale = nullptr;
   int32_t *lens, *table = nullptr;
-  Cache(PyObject* k_, PyObject* v_, PyObject* ks_, PyObject* vs_, PyObject* lens_, PyObject* table_, int B, int d,
-        int dev) {
+  Cache(bool fp8, PyObject* k_, PyObject* v_, PyObject* ks_, PyObject* vs_, PyObject* lens_, PyObject* table_, int B,
+        int d, int dev) {
     const at::Tensor &tk = tensor(k_, "k_cache"), &tv = tensor(v_, "v_cache"), &tl = tensor(lens_, "lengths");
     if (tk.dim() != 4 || tv.sizes() != tk.sizes() || tk.size(3) != d || tl.dim() != 1 || tl.size(0) != B)
       refuse("shape mismatch");
-    fp8 = ks_ != Py_None;
     Hkv = dim(tk.size(2));
-    k = cache(tk, "k_cache", fp8, dev);
-    v = cache(tv, "v_cache", fp8, dev);
-    lens = static_cast<int32_t*>(typed(lens_, "lengths", at::kInt, dev));
     if (fp8) {
       const at::Tensor &ts = tensor(ks_, "k_scale"), &tw = tensor(vs_, "v_scale");
       if (ts.dim() != 1 || ts.size(0) != Hkv || tw.sizes() != ts.sizes()) refuse("k_scale and v_scale must be [Hkv]");
       k_scale = static_cast<float*>(typed(ks_, "k_scale", at::kFloat, dev));
       v_scale = static_cast<float*>(typed(vs_, "v_scale", at::kFloat, dev));
     }
+    k = cache(tk, "k_cache", fp8, dev);
+    v = cache(tv, "v_cache", fp8, dev);
+    lens = static_cast<int32_t*>(typed(lens_, "lengths", at::kInt, dev));
     if (table_ == Py_None) {
       if (tk.size(0) != B) refuse("a contiguous cache must be [B, capacity, Hkv, d]");
       capacity = dim(tk.size(1));
@@ -221,7 +219,7 @@ int prefill_window(PyObject* const* a) {
 int prefill_cache_window(PyObject* const* a) {
   const int dev = i32(a[0]);
   const Queries q(a[2], a[6], a[9], dev);
-  const Cache c(a[3], a[4], Py_None, Py_None, a[5], a[10], q.B, q.d, dev);
+  const Cache c(false, a[3], a[4], Py_None, Py_None, a[5], a[10], q.B, q.d, dev);
   const int window = i32(a[7]), sinks = i32(a[8]);
   const float scale = scale_or_default(a[11], q.d);
   void* stream = stream_of(a[1]);
@@ -232,16 +230,17 @@ int prefill_cache_window(PyObject* const* a) {
 
 // (dev, stream, q, k_cache, v_cache, k_scale, v_scale, seqlens, o, window, sinks, lse, page_table, max_seqlen_k,
 //  scale, num_splits, workspace)
+template <bool FP8>
 int decode_window(PyObject* const* a) {
   const int dev = i32(a[0]);
   const Queries q(a[2], a[8], a[11], dev);
-  const Cache c(a[3], a[4], a[5], a[6], a[7], a[12], q.B, q.d, dev);
+  const Cache c(FP8, a[3], a[4], a[5], a[6], a[7], a[12], q.B, q.d, dev);
   const Workspace w(a[16], dev);
   const int window = i32(a[9]), sinks = i32(a[10]), longest = i32(a[13]), splits = i32(a[15]);
   const float scale = scale_or_default(a[14], q.d);
   void* stream = stream_of(a[1]);
   const NoGil free;
-  if (c.fp8)
+  if (FP8)
     return attn_decode_window_fp8(q.q, c.k, c.v, c.k_scale, c.v_scale, c.lens, c.table, c.max_blocks, c.num_blocks,
                                   c.capacity, longest, q.o, q.o_type, q.lse, q.B, q.T, q.Hq, c.Hkv, q.d, scale, window,
                                   sinks, splits, w.p, w.n, stream);
@@ -252,11 +251,12 @@ int decode_window(PyObject* const* a) {
 
 // (dev, stream, q, k_cache, v_cache, k_scale, v_scale, seqlens, page_table, prefix_table, o, lse, max_seqlen_k,
 //  scale, causal, num_splits, workspace)
+template <bool FP8>
 int decode_shared(PyObject* const* a) {
   const int dev = i32(a[0]);
   if (a[8] == Py_None) refuse("a shared prefix needs a page table");
   const Queries q(a[2], a[10], a[11], dev);
-  const Cache c(a[3], a[4], a[5], a[6], a[7], a[8], q.B, q.d, dev);
+  const Cache c(FP8, a[3], a[4], a[5], a[6], a[7], a[8], q.B, q.d, dev);
   const at::Tensor& prefix = tensor(a[9], "prefix_table");
   if (prefix.dim() != 1) refuse("prefix_table must be [prefix_blocks]");
   const int n = dim(prefix.size(0));
@@ -266,7 +266,7 @@ int decode_shared(PyObject* const* a) {
   const float scale = scale_or_default(a[13], q.d);
   void* stream = stream_of(a[1]);
   const NoGil free;
-  if (c.fp8)
+  if (FP8)
     return attn_decode_shared_fp8(q.q, c.k, c.v, c.k_scale, c.v_scale, c.lens, c.table, c.max_blocks, c.num_blocks,
                                   pre, n, longest, q.o, q.o_type, q.lse, q.B, q.T, q.Hq, c.Hkv, q.d, scale, causal,
                                   splits, w.p, w.n, stream);
@@ -298,13 +298,14 @@ int norm_rope(PyObject* const* a) {
 
 // (dev, stream, k_cache, v_cache, q, k_new, v_new, q_out, k_scale, v_scale, rope, cache_lens, page_table, q_weight,
 //  k_weight, eps, interleaved)
+template <bool FP8>
 int append_norm_rope(PyObject* const* a) {
   const int dev = i32(a[0]);
   const at::Tensor &tq = tensor(a[4], "q"), &tk = tensor(a[5], "k_new"), &tv = tensor(a[6], "v_new");
   if (tq.dim() != 4 || tk.dim() != 4 || tv.sizes() != tk.sizes() || tensor(a[7], "q_out").sizes() != tq.sizes())
     refuse("shape mismatch");
   const int B = dim(tq.size(0)), T = dim(tq.size(1)), Hq = dim(tq.size(2)), d = dim(tq.size(3));
-  const Cache c(a[2], a[3], a[8], a[9], a[11], a[12], B, d, dev);
+  const Cache c(FP8, a[2], a[3], a[8], a[9], a[11], a[12], B, d, dev);
   if (tk.size(2) != c.Hkv) refuse("shape mismatch");
   const Rows q(a[4], "q", B, T, d, dev), k(a[5], "k_new", B, T, d, dev), v(a[6], "v_new", B, T, d, dev);
   const Turn t(a[13], a[14], a[10], d, dev);
@@ -313,7 +314,7 @@ int append_norm_rope(PyObject* const* a) {
   const int interleaved = truth(a[16]);
   void* stream = stream_of(a[1]);
   const NoGil free;
-  if (c.fp8)
+  if (FP8)
     return kv_append_norm_rope_fp8(c.k, c.v, q.p, k.p, v.p, q.stride, k.stride, v.stride, q_out, c.k_scale, c.v_scale,
                                    t.qw, t.kw, eps, t.rope, t.rows, t.rot, interleaved, c.lens, c.table, c.max_blocks,
                                    c.num_blocks, c.capacity, B, T, Hq, c.Hkv, d, stream);
@@ -338,9 +339,16 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
 }
 
-#define FAST(name, args) {#name, (PyCFunction)(void (*)(void))call<name, args>, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(prefill_window, 10),   FAST(prefill_cache_window, 12), FAST(decode_window, 17),
-                         FAST(decode_shared, 17),    FAST(norm_rope, 12),            FAST(append_norm_rope, 17),
+#define FAST(name, function, args) {name, (PyCFunction)(void (*)(void))call<function, args>, METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {FAST("prefill_window", prefill_window, 10),
+                         FAST("prefill_cache_window", prefill_cache_window, 12),
+                         FAST("decode_window", decode_window<false>, 17),
+                         FAST("decode_window_fp8", decode_window<true>, 17),
+                         FAST("decode_shared", decode_shared<false>, 17),
+                         FAST("decode_shared_fp8", decode_shared<true>, 17),
+                         FAST("norm_rope", norm_rope, 12),
+                         FAST("append_norm_rope", append_norm_rope<false>, 17),
+                         FAST("append_norm_rope_fp8", append_norm_rope<true>, 17),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

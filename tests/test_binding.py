@@ -62,7 +62,7 @@ def test_calls_allocate_on_the_stream_they_launch_on(monkeypatch, call, stream, 
     kernels still write their partials to it."""
     made = Allocations(monkeypatch)
     monkeypatch.setattr(kv, "lib", Launches())
-    monkeypatch.setattr(kv, "_marshal", types.SimpleNamespace(decode_window=lambda *a: 0, decode_shared=lambda *a: 0))
+    monkeypatch.setattr(kv, "_marshal", Launches())
     monkeypatch.setattr(kv, "_here", lambda t, s: (0, s or 0))
     monkeypatch.setattr(kv, "_dev", lambda *a: 0)
     monkeypatch.setattr(kv, "_codes", lambda *a: 0)

@@ -277,3 +277,24 @@ def test_invalid_lengths_are_flagged_by_plain_decode_too(kind, T, Hq, Hkv, num_s
         assert kv.attn_get_device_status(clear=True) == kv.ATTN_DEV_SEQLEN
         assert torch.isnan(o[bad]).all() and torch.isnan(lse[bad]).all()
         assert torch.isfinite(o[1 - bad]).all() and torch.isfinite(lse[1 - bad]).all()
+
+
+# ------------------------------------------------------------------- arguments of the wrong kind
+@pytest.mark.parametrize("missing", ["k_scale", "v_scale", "both"])
+def test_fp8_calls_need_their_scales(missing):
+    """Without scales an FP8 call is refused, over a bf16 cache too: it would run as the bf16 call."""
+    q = torch.zeros(1, 1, 4, 128, dtype=torch.bfloat16, device="cuda")
+    o, n, table = torch.zeros(1, 1, 4, 128, device="cuda"), to_dev_i32([5]), to_dev_i32([[0, 1]])
+    new = torch.zeros(1, 1, 2, 128, dtype=torch.bfloat16, device="cuda")
+    scale = torch.ones(2, device="cuda")
+    ks, vs = None if missing != "v_scale" else scale, None if missing != "k_scale" else scale
+    for dtype in (torch.bfloat16, torch.uint8):
+        c = torch.zeros(2, 16, 2, 128, dtype=dtype, device="cuda")
+        calls = [lambda: kv.attn_decode_window_fp8(q, c, c, ks, vs, n, o, 3, page_table=table),
+                 lambda: kv.attn_decode_shared_fp8(q, c, c, ks, vs, to_dev_i32([20]), table, table[0, :1], o),
+                 lambda: kv.kv_append_norm_rope_fp8(c, c, q, new, new, torch.zeros_like(q), ks, vs, None, n,
+                                                    page_table=table)]
+        for call in calls:
+            with pytest.raises(ValueError, match="scale"):
+                call()
+        assert not c.any() and not o.any()
