@@ -41,6 +41,7 @@ void* typed(PyObject* o, const char* name, ScalarType type, int dev) {
   return place(t, name, dev);
 }
 
+// None: no pointer.  An empty tensor has none either, so who asks for shapes asks for None, not for the pointer.
 void* optional(PyObject* o, const char* name, ScalarType type, int dev) {
   return o == Py_None ? nullptr : typed(o, name, type, dev);
 }
@@ -109,7 +110,7 @@ struct Queries {
     o = place(to, "o", dev);
     o_type = out_type(to);
     lse = static_cast<float*>(optional(lse_, "lse", at::kFloat, dev));
-    if (lse) {
+    if (lse_ != Py_None) {
       const at::Tensor& tl = THPVariable_Unpack(lse_);
       if (tl.dim() != 3 || tl.size(0) != B || tl.size(1) != Hq || tl.size(2) != T) refuse("lse must be [B, Hq, T]");
     }
@@ -191,9 +192,9 @@ struct Turn {
       if (w != Py_None && (THPVariable_Unpack(w).dim() != 1 || THPVariable_Unpack(w).size(0) != d))
         refuse("q_weight and k_weight must be [d]");
     rope = static_cast<float*>(optional(rope_, "rope", at::kFloat, dev));
-    if (rope) {
+    if (rope_ != Py_None) {
       const at::Tensor& t = THPVariable_Unpack(rope_);
-      if (t.dim() != 2) refuse("rope must be [rows, rot_dim]");
+      if (t.dim() != 2 || t.numel() == 0) refuse("rope must be [rows, rot_dim]");
       rows = dim(t.size(0));
       rot = dim(t.size(1));
     }
@@ -285,7 +286,7 @@ int norm_rope(PyObject* const* a) {
   const Rows q(a[2], "q", B, T, d, dev), k(a[3], "k", B, T, d, dev);
   const Turn t(a[7], a[8], a[6], d, dev);
   const int32_t* pos0 = static_cast<int32_t*>(optional(a[11], "pos0", at::kInt, dev));
-  if (pos0 && (THPVariable_Unpack(a[11]).dim() != 1 || THPVariable_Unpack(a[11]).size(0) != B))
+  if (a[11] != Py_None && (THPVariable_Unpack(a[11]).dim() != 1 || THPVariable_Unpack(a[11]).size(0) != B))
     refuse("pos0 must be [B]");
   void *q_out = typed(a[4], "q_out", at::kBFloat16, dev), *k_out = typed(a[5], "k_out", at::kBFloat16, dev);
   const int Hkv = dim(tk.size(2)), interleaved = truth(a[10]);

@@ -298,3 +298,20 @@ def test_fp8_calls_need_their_scales(missing):
             with pytest.raises(ValueError, match="scale"):
                 call()
         assert not c.any() and not o.any()
+
+
+def test_empty_tensors_are_not_none():
+    """An empty pos0, angle table or lse is a mistake of shape, not the default."""
+    q = torch.ones(1, 2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    out, rope = torch.zeros_like(q), kv.rope_table(8, 64)
+    nothing = torch.empty(0, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="pos0"):
+        kv.qk_norm_rope(q, q, out, torch.zeros_like(q), rope, pos0=nothing)
+    for shape in ((0, 64), (8, 0), (0, 0)):
+        with pytest.raises(ValueError, match="rope"):
+            kv.qk_norm_rope(q, q, out, torch.zeros_like(q), torch.empty(shape, device="cuda"))
+    o = torch.zeros(1, 2, 4, 64, device="cuda")
+    for shape in ((0,), (1, 4, 0), (0, 4, 2)):
+        with pytest.raises(ValueError, match="lse"):
+            kv.attn_prefill_window(q, q, q, o, 3, lse=torch.empty(shape, device="cuda"))
+    assert not out.any() and not o.any()
