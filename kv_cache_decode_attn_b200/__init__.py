@@ -17,6 +17,7 @@ import contextlib
 import ctypes
 import math
 import os
+import sysconfig
 
 import torch
 
@@ -115,11 +116,20 @@ def _load() -> ctypes.CDLL:
     return handle
 
 
+def _load_marshal():
+    try:
+        from . import _marshal as module
+    except ImportError as e:
+        raise ImportError(f"{e}: build the package with `python kv_cache_decode_attn_b200/build.py`") from e
+    here = f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+    if module.built_for != here:
+        raise ImportError(f"_marshal.so was built for {module.built_for}, this is {here}: build it again with "
+                          "`python kv_cache_decode_attn_b200/build.py`")
+    return module
+
+
 lib = _load()
-try:
-    from . import _marshal  # noqa: E402
-except ImportError as e:
-    raise ImportError(f"{e}: build the package with `python kv_cache_decode_attn_b200/build.py`") from e
+_marshal = _load_marshal()
 
 
 class AttnError(RuntimeError):

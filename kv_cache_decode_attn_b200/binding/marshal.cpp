@@ -355,4 +355,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__marshal(void) {
+  PyObject* m = PyModule_Create(&module);
+  // the torch and Python whose headers this was compiled against
+  if (m && PyModule_AddStringConstant(m, "built_for", KVATTN_BUILT_FOR)) Py_CLEAR(m);
+  return m;
+}

@@ -6,16 +6,19 @@ the CUDA runtime statically and reaches the driver API (tensor-map encoding)
 through ``cudaGetDriverEntryPointByVersion``, so it needs no ``-lcuda`` at link
 time.  ``binding/marshal.cpp`` (argument checks of the Python binding, compiled against
 the installed torch's headers) becomes ``_marshal.so``, which calls the library beside it.
-Rebuilds only when a source is newer than what it makes.
+Rebuilds only when a source is newer than what it makes, and the binding also for another
+torch or Python than it was built for: both have C++ and C interfaces of their own.
 """
 
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -23,6 +26,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libkvattn.so")
 BINDING = os.path.join(HERE, "binding", "marshal.cpp")
 MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL_KEY = os.path.join(HERE, "_build", "marshal.key")   # what MARSHAL was built for
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -50,13 +54,24 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
-def build_binding(force: bool = False, verbose: bool = False) -> str:
-    header = os.path.join(INCLUDE, "attn.h")
-    if not force and os.path.exists(MARSHAL) and \
-            os.path.getmtime(MARSHAL) > max(os.path.getmtime(BINDING), os.path.getmtime(header)):
-        return MARSHAL
-    import sysconfig
+def binding_key() -> str:
+    """The torch and Python that a binding built now is for; the package compares it when it is imported."""
+    return f"torch {importlib.metadata.version('torch')}, {sysconfig.get_config_var('SOABI')}"
 
+
+def _binding_stale() -> bool:
+    if not os.path.exists(MARSHAL) or not os.path.exists(MARSHAL_KEY):
+        return True
+    with open(MARSHAL_KEY) as f:
+        if f.read() != binding_key():
+            return True
+    t = os.path.getmtime(MARSHAL)
+    return any(os.path.getmtime(p) >= t for p in (BINDING, os.path.join(INCLUDE, "attn.h")))
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    if not force and not _binding_stale():
+        return MARSHAL
     import torch
     from torch.utils import cpp_extension
 
@@ -64,13 +79,17 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     inc += [f"-isystem{d}" for d in cpp_extension.include_paths()]
     tmp = MARSHAL + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, BINDING, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DKVATTN_BUILT_FOR="{binding_key()}"', *inc, BINDING, "-o", tmp,
            f"-L{HERE}", "-l:libkvattn.so", "-Wl,-rpath,$ORIGIN",
            *(f"-L{d}" for d in cpp_extension.library_paths()), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, MARSHAL)
+    os.makedirs(os.path.dirname(MARSHAL_KEY), exist_ok=True)
+    with open(MARSHAL_KEY, "w") as f:
+        f.write(binding_key())
     return MARSHAL
 
 

@@ -1,6 +1,8 @@
 """The Python binding's own behaviour, without a GPU: CUDA calls, streams and allocations are stand-ins."""
 
 import contextlib
+import importlib.util
+import os
 import types
 
 import pytest
@@ -70,3 +72,50 @@ def test_calls_allocate_on_the_stream_they_launch_on(monkeypatch, call, stream, 
     monkeypatch.setattr(kv, "_raw_stream", None)
     call(stream)
     assert made.on == [used]
+
+
+def build_script():
+    path = os.path.join(os.path.dirname(kv.__file__), "build.py")
+    spec = importlib.util.spec_from_file_location("kvattn_build_under_test", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+def test_the_binding_is_built_again_for_another_torch_or_python(monkeypatch, tmp_path):
+    """The compiled binding is of one torch's and one Python's interface, whatever the files' times say."""
+    b = build_script()
+    monkeypatch.setattr(b, "MARSHAL", str(tmp_path / "_marshal.so"))
+    monkeypatch.setattr(b, "MARSHAL_KEY", str(tmp_path / "key"))
+    built = []
+
+    def compiler(cmd, check):
+        built.append([a for a in cmd if a.startswith("-DKVATTN_BUILT_FOR")])
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    monkeypatch.setattr(b.subprocess, "run", compiler)
+    b.build_binding()
+    b.build_binding()
+    assert len(built) == 1 and built[0] == [f'-DKVATTN_BUILT_FOR="{b.binding_key()}"']
+    version = b.importlib.metadata.version
+    monkeypatch.setattr(b.importlib.metadata, "version", lambda name: "9.9" if name == "torch" else version(name))
+    b.build_binding()
+    b.build_binding()
+    assert len(built) == 2 and "torch 9.9" in built[1][0]
+    config = b.sysconfig.get_config_var
+    monkeypatch.setattr(b.sysconfig, "get_config_var", lambda name: "cpython-399" if name == "SOABI" else config(name))
+    b.build_binding()
+    assert len(built) == 3
+    os.utime(b.MARSHAL, (1, 1))     # older than its sources
+    b.build_binding()
+    assert len(built) == 4
+    os.remove(b.MARSHAL_KEY)
+    b.build_binding()
+    assert len(built) == 5
+
+
+def test_a_binding_of_another_torch_is_refused(monkeypatch):
+    assert kv._marshal.built_for.startswith(f"torch {torch.__version__}")
+    monkeypatch.setattr(torch, "__version__", "1.0")
+    with pytest.raises(ImportError, match="torch 1.0"):
+        kv._load_marshal()
