@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int hh = 0; hh < C::kHalves; ++hh)
-              tma_prefetch_4d(&tmQ, hh * 64, nx.h, (2 * nx.qb + t) * kBM, nx.b);
+              tma_prefetch_4d(&tmQ, hh * 64, nx.h, ((WIN ? p.item_tiles : 2) * nx.qb + t) * kBM, nx.b);
         }
       }
     }

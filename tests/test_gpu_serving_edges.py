@@ -315,3 +315,21 @@ def test_empty_tensors_are_not_none():
         with pytest.raises(ValueError, match="lse"):
             kv.attn_prefill_window(q, q, q, o, 3, lse=torch.empty(shape, device="cuda"))
     assert not out.any() and not o.any()
+
+
+def test_items_of_one_query_tile_follow_one_another():
+    """A windowed prefill of fewer one-tile items than SMs, beside a long one that holds the SMs: its CTAs then
+    take several items each."""
+    long = synth.prefill_inputs(4, 32, 8, 4096, 128, seed=6, device="cuda")
+    lo = torch.empty_like(long[0])
+    q, k, v = synth.prefill_inputs(1, 14, 2, 1200, 128, seed=7, device="cuda")       # 5 x 14 x 2 <= 148
+    want = torch.empty_like(q, dtype=torch.float32)
+    kv.attn_prefill_window(q, k, v, want, 300, 4)
+    outs = [torch.full_like(want, float("nan")) for _ in range(6)]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for o in outs:
+        kv.attn_prefill(*long, lo, stream=a)
+        kv.attn_prefill_window(q, k, v, o, 300, 4, stream=b)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
