@@ -1092,16 +1092,7 @@ cudaError_t launch_decode_combine(const DecodeLaunch& a, cudaStream_t stream) {
   // chunks took 29 us with 8 warps a row, seven waves that each wait for their loads
   const long long warps = a.sel.select ? 16LL * device_sms() : INT64_MAX;
   while (wpr < 8 && wpr * 4 < row_chunks && rows_out * wpr * 2 <= warps) wpr *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((rows_out * wpr + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  const dim3 grid((unsigned)((rows_out * wpr + 7) / 8));
   const int paged_i = a.page_table != nullptr ? 1 : 0;
   const bool light = row_chunks <= 2;
   const PrefixParts pre = {a.pre_o, a.pre_lse, a.pre_chunks, a.B * sp.R, a.pre_stream, a.pre_tiles};
@@ -1111,10 +1102,8 @@ cudaError_t launch_decode_combine(const DecodeLaunch& a, cudaStream_t stream) {
                       : (light ? decode_combine_kernel<64, 2, S> : decode_combine_kernel<64, 8, S>);
   };
   auto kern = a.sel.select ? pick(std::true_type{}) : pick(std::false_type{});
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, (const float*)a.part_o, (const float*)a.part_lse, a.seqlens, a.o, a.o_bf16,
-                         a.lse, sp, a.B, paged_i, wpr, pre);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return launch_beside(kern, grid, 256, 0, stream, (const float*)a.part_o, (const float*)a.part_lse, a.seqlens, a.o,
+                       a.o_bf16, a.lse, sp, a.B, paged_i, wpr, pre);
 }
 
 }  // namespace kvattn

@@ -873,7 +873,7 @@ cudaError_t run_tc_as(const DecodeLaunch& a, const CUtensorMap& tk, const CUtens
   if (a.balanced) grid = dim3((unsigned)a.n_chunks * a.Hkv);
   if constexpr (SEL) {
     grid.x += a.fence;
-    return launch_beside(kern, grid, tc_threads<FP8>(), C::kSmemBytes, stream, true, tq, tk, tv, p);
+    return launch_beside(kern, grid, tc_threads<FP8>(), C::kSmemBytes, stream, tq, tk, tv, p);
   }
   kern<<<grid, tc_threads<FP8>(), C::kSmemBytes, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();

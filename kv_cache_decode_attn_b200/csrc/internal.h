@@ -80,10 +80,10 @@ struct KeySelect {
   int fixed_len = 0;   // > 0: every sequence has exactly this many keys (seqlens is not read)
 };
 
-// Launch a kernel.  `beside`: its CTAs may start before the kernel in front of it in the
-// stream has ended (programmatic dependent launch); it waits itself, where it has to.
+// Launch a kernel whose CTAs may start before the kernel in front of it in the stream has
+// ended (programmatic dependent launch); it waits itself, where it has to.
 template <class Kernel, class... Args>
-inline cudaError_t launch_beside(Kernel kern, dim3 grid, int threads, int smem, cudaStream_t stream, bool beside,
+inline cudaError_t launch_beside(Kernel kern, dim3 grid, int threads, int smem, cudaStream_t stream,
                                  const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -94,7 +94,7 @@ inline cudaError_t launch_beside(Kernel kern, dim3 grid, int threads, int smem, 
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = beside ? 1 : 0;
+  cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

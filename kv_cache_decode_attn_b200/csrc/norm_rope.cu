@@ -300,7 +300,7 @@ cudaError_t run_norm_rope(const NormRopeLaunch& a, int head_groups, cudaStream_t
   const int head_blocks = (head_groups + 7) / 8, warps = (head_groups + head_blocks - 1) / head_blocks;
   if (token_groups * head_blocks > INT32_MAX) return cudaErrorInvalidValue;
   return launch_beside(norm_rope_kernel<D, kTokens, CACHED, FP8>, dim3((unsigned)(token_groups * head_blocks)),
-                       32 * warps, 0, stream, true, a, head_blocks);
+                       32 * warps, 0, stream, a, head_blocks);
 }
 
 template <int D, bool CACHED, bool FP8>

@@ -1004,7 +1004,7 @@ cudaError_t run_prefill(const PrefillLaunch& a, cudaStream_t stream) {
     return cudaErrorInvalidConfiguration;
   // one CTA per SM runs at a time (each owns all 512 TMEM columns)
   const unsigned grid = (unsigned)items;
-  if constexpr (WIN) return launch_beside(kern, dim3(grid), kThreads, C::kSmemBytes, stream, true, tq, tk, tv, p);
+  if constexpr (WIN) return launch_beside(kern, dim3(grid), kThreads, C::kSmemBytes, stream, tq, tk, tv, p);
   kern<<<grid, kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }

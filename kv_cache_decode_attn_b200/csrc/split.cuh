@@ -413,7 +413,7 @@ template <class Kernel>
 inline cudaError_t launch_sel(Kernel kern, int threads, int smem, const CUtensorMap& tk, const CUtensorMap& tv,
                               const SplitParams& sp, int B, cudaStream_t stream) {
   const dim3 grid = sp.stream ? dim3(sp.stream * sp.Hkv + sp.fence) : dim3(sp.max_chunks + sp.fence, sp.Hkv, B);
-  return launch_beside(kern, grid, threads, smem, stream, true, tk, tv, sp);
+  return launch_beside(kern, grid, threads, smem, stream, tk, tv, sp);
 }
 
 // FP8 caches, at most 8 query rows per KV head: the transposed-product split kernel (decode_fp8.cu)
