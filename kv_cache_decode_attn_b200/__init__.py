@@ -411,9 +411,12 @@ def decode_window_workspace(B, T, Hq, Hkv, d, max_seqlen_k, window, sinks=0, num
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _longest(k_cache, page_table, max_seqlen_k) -> int:
-    """The bound on the lengths: max_seqlen_k, or the cache's capacity where that is 0."""
-    return max_seqlen_k or int(k_cache.shape[1] if page_table is None else page_table.shape[1] * 16)
+def _decode_sizes(q, k_cache, page_table, max_seqlen_k):
+    """(B, T, Hq, Hkv, d, the bound on the lengths: max_seqlen_k, or the cache's capacity where that is 0)."""
+    if q.dim() != 4 or k_cache.dim() != 4 or (page_table is not None and page_table.dim() != 2):
+        raise ValueError("shape mismatch")
+    longest = max_seqlen_k or int(k_cache.shape[1] if page_table is None else page_table.shape[1] * 16)
+    return (*q.shape[:3], k_cache.shape[2], q.shape[3], longest)
 
 
 def attn_decode_window(q, k_cache, v_cache, seqlens_k, o, window, sinks=0, lse=None, page_table=None, max_seqlen_k=0,
@@ -423,9 +426,8 @@ def attn_decode_window(q, k_cache, v_cache, seqlens_k, o, window, sinks=0, lse=N
     here = _here(q, stream)
     if workspace is None:
         with _allocating_on(stream, q.device):
-            workspace = decode_window_workspace(*q.shape[:3], k_cache.shape[2], q.shape[3],
-                                                _longest(k_cache, page_table, max_seqlen_k), window, sinks, num_splits,
-                                                q.device)
+            workspace = decode_window_workspace(*_decode_sizes(q, k_cache, page_table, max_seqlen_k), window, sinks,
+                                                num_splits, q.device)
     st = _marshal.decode_window(*here, q, k_cache, v_cache, None, None, seqlens_k, o, window, sinks, lse, page_table,
                                 max_seqlen_k, scale, num_splits, workspace)
     _check("attn_decode_window", st)
@@ -438,9 +440,8 @@ def attn_decode_window_fp8(q, k_cache, v_cache, k_scale, v_scale, seqlens_k, o, 
     here = _here(q, stream)
     if workspace is None:
         with _allocating_on(stream, q.device):
-            workspace = decode_window_workspace(*q.shape[:3], k_cache.shape[2], q.shape[3],
-                                                _longest(k_cache, page_table, max_seqlen_k), window, sinks, num_splits,
-                                                q.device)
+            workspace = decode_window_workspace(*_decode_sizes(q, k_cache, page_table, max_seqlen_k), window, sinks,
+                                                num_splits, q.device)
     st = _marshal.decode_window_fp8(*here, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, o, window, sinks, lse,
                                     page_table, max_seqlen_k, scale, num_splits, workspace)
     _check("attn_decode_window_fp8", st)
@@ -462,14 +463,15 @@ def decode_shared_workspace(B, T, Hq, Hkv, d, max_seqlen_k, prefix_blocks, num_s
 
 def _decode_shared(name, marshal, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_table, prefix_table, o, lse,
                    max_seqlen_k, scale, causal, num_splits, workspace, stream) -> None:
+    if page_table is None or prefix_table is None:
+        raise ValueError("a shared prefix needs a page table and a prefix table")
     here = _here(q, stream)
     if workspace is None:
-        if page_table is None:
-            raise ValueError("a shared prefix needs a page table")
+        if prefix_table.dim() != 1:
+            raise ValueError("prefix_table must be [prefix_blocks]")
         with _allocating_on(stream, q.device):
-            workspace = decode_shared_workspace(*q.shape[:3], k_cache.shape[2], q.shape[3],
-                                                _longest(k_cache, page_table, max_seqlen_k), prefix_table.shape[0],
-                                                num_splits, q.device)
+            workspace = decode_shared_workspace(*_decode_sizes(q, k_cache, page_table, max_seqlen_k),
+                                                prefix_table.shape[0], num_splits, q.device)
     st = marshal(*here, q, k_cache, v_cache, k_scale, v_scale, seqlens_k, page_table, prefix_table, o, lse,
                  max_seqlen_k, scale, causal, num_splits, workspace)
     _check(name, st)

@@ -119,3 +119,20 @@ def test_a_binding_of_another_torch_is_refused(monkeypatch):
     monkeypatch.setattr(torch, "__version__", "1.0")
     with pytest.raises(ImportError, match="torch 1.0"):
         kv._load_marshal()
+
+
+def test_shapes_are_refused_by_value_without_a_workspace(monkeypatch):
+    """The sizes of the call's own workspace come from the arguments before the compiled checks see them."""
+    monkeypatch.setattr(kv, "_here", lambda t, s: (0, 0))
+    for q, cache, table, prefix in [(_q[0], _pool, _table, _prefix), (_q, _pool[0], _table, _prefix),
+                                    (_q, _pool, _table[0], _prefix), (_q, _pool, None, _prefix),
+                                    (_q, _pool, _table, None), (_q, _pool, _table, _prefix[None])]:
+        with pytest.raises(ValueError):
+            kv.attn_decode_shared(q, cache, cache, _n, table, prefix, _o)
+        with pytest.raises(ValueError):
+            kv.attn_decode_shared_fp8(q, cache, cache, _scale, _scale, _n, table, prefix, _o)
+    for q, cache, table in [(_q[0], _cache, None), (_q, _cache[0], None), (_q, _pool, _table[0])]:
+        with pytest.raises(ValueError):
+            kv.attn_decode_window(q, cache, cache, _n, _o, 9, page_table=table)
+        with pytest.raises(ValueError):
+            kv.attn_decode_window_fp8(q, cache, cache, _scale, _scale, _n, _o, 9, page_table=table)
