@@ -21,7 +21,11 @@
  *   - GQA/MQA: query head h reads K/V head h / (Hq / Hkv) ([P5] "GQA im leicht
  *     lesbaren Code": repeat_interleave along the head axis).  Hq % Hkv == 0.
  *   - Head dimension d is 64 or 128.
- *   - LSE outputs are natural-log log-sum-exp of the SCALED scores, fp32.
+ *   - LSE outputs are natural-log log-sum-exp of the SCALED scores, fp32; NaN where
+ *     a score the row sees is NaN.
+ *   - Cached keys and values that no query of a call sees may hold anything, NaN and
+ *     infinities too.  What some of its queries see and others do not must be finite
+ *     in V: a masked weight is an exact 0, and 0 times such a value is NaN.
  *   - Paged caches ([P1] "页面注意 KV缓存作为虚拟内存"): pools of 16-token physical
  *     blocks laid out [num_blocks, 16, Hkv, d]; a page table int32
  *     [B, max_blocks_per_seq] maps logical block j/16 of sequence b to a

@@ -995,6 +995,11 @@ bool decode_direct(long long units, int max_keys, bool tc) {
   // products); with more CTAs than SMs the tiles of two share the SM's bandwidth; and the partials
   // and the combine of a split.  16 x 8 pairs with a window of 1024: 14.5 us a call against 19.7
   // split; 1 x 8 pairs: 11.6 against 8.7.
+  // Held against both sides in 108 calls (bf16 at d = 64 and 128, FP8; 4 to 64 rows per KV head; 16,
+  // 128 and 320 units; windows of 256, 1024, 4096): within 3 % of the faster one in 72, 10 % in 80.
+  // The others are split where whole is faster: more units than two CTAs per SM hold, with windows
+  // up to 1024 (320 units, 256 keys: 4 FP8 rows 16.6 us and 9.5 whole, 64 bf16 rows 43.6 and 25.0), and
+  // the tensor-core kernel with few units or 1024 keys (16 units, 256 keys, 64 rows: 14.3 and 10.9).
   const double tiles = (max_keys + kDecodeTile - 1) / kDecodeTile, sms = device_sms(), tile = tc ? 1.3 : 0.65;
   const double waves = units <= sms ? 1.0 : 1.7 * ceil(units / (2 * sms));
   return tiles * tile * waves <= tiles * 0.55 * units / sms + 5.0;
@@ -1003,8 +1008,12 @@ bool decode_direct(long long units, int max_keys, bool tc) {
 bool decode_shared_together(int B, int T, int G, int Hkv, int max_seqlen, int prefix, bool fp8) {
   // us on B200, as in decode_direct (0.55 a tile with two CTAs per SM, 1.0 on the tensor-core kernel,
   // 8 to start, split and merge), against the three launches of the shared form: 4 sequences behind
-  // 1024 tokens 11.1 us instead of 14.2, 40 behind 256 tokens 8.6 instead of 13.8.  Not on the
+  // 1024 tokens 11.1 us instead of 14.3, 40 behind 256 tokens 8.6 instead of 13.8.  Not on the
   // tensor-core kernel: the lookup there slowed every shared call (94 to 99 us behind 32768 tokens).
+  // Held against both sides in 54 calls (bf16 at d = 64 and 128, FP8; 4 and 16 rows per KV head; 4, 12 and
+  // 40 sequences behind 256, 1024 and 4096 tokens): within 3 % of the faster one in 43, 12 % in 49; the
+  // worst are 4 sequences of 4 rows behind 4096 (20.6 us, read by each 15.5) and of 16 rows behind 1024
+  // (20.9, three launches 16.4).
   const int rows = G * T;
   if (decode_uses_tc(rows, fp8)) return false;
   const double sms = device_sms();

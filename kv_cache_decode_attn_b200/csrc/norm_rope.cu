@@ -18,7 +18,8 @@
 // 4 x 4096 tokens of 32 + 8 + 8 heads (405 MB; 62 us at the copy rate): 93 us with one
 // token per warp, indexes divided out per row and single fp32 operations (issue slots
 // 72 % busy); 98 with the angles read per token by each warp (waiting for them);
-// 80 as it is, with three CTAs per SM (99 without that bound on the registers).
+// 80 as it is, with three CTAs per SM (99 without that bound on the registers); 81 to 87
+// from one B200 to another.
 #include <cuda_bf16.h>
 #include <math.h>
 
