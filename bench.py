@@ -254,10 +254,10 @@ def decode_kernel(wd):
             return "decode_fp8_st_kernel", ("decode_fp8.cu", "split.cuh", "decode.cu")
         if R <= 32:
             return "decode_split_kernel<fp8>", ("decode.cu", "split.cuh")
-        return "decode_tc_kernel<fp8>", ("decode_tc.cu", "decode.cu")
+        return "decode_tc_kernel<fp8>", ("decode_tc.cu", "decode.cu", "split.cuh")
     if R <= 16:
         return "decode_split_kernel", ("decode.cu", "split.cuh")
-    return "decode_tc_kernel", ("decode_tc.cu", "decode.cu")
+    return "decode_tc_kernel", ("decode_tc.cu", "decode.cu", "split.cuh")
 
 
 def run_ours(args, world, rank, local):
