@@ -429,3 +429,81 @@ def test_calls_repeat_their_bits():
         torch.cuda.synchronize()
         first = first or got
         assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
+# -------------------------------------------------------------------- offsets that do not fit in 32 bits
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_far_into_a_large_pool(fp8):
+    """Blocks of a pool whose last elements lie past 2^31 elements and 2^32 bytes: written by the append, read by
+    windowed and shared-prefix decode and by a windowed chunk."""
+    B, Hq, Hkv, d = 3, 16, 8, 128
+    total = (1 << (18 if fp8 else 17)) + 300          # blocks of 16 * 8 * 128 elements
+    dtype = torch.uint8 if fp8 else torch.bfloat16
+    pools = [torch.zeros(total, 16, Hkv, d, dtype=dtype, device="cuda") for _ in "kv"]
+    scales = [torch.full((Hkv,), s, device="cuda") for s in (0.03, 0.02)] if fp8 else []
+    blocks, shared_blocks, T = 40, 20, 280
+    table = torch.stack([torch.cat([torch.arange(total - 1, total - 1 - shared_blocks, -1),
+                                    torch.arange(blocks - shared_blocks) + total - 200 + 60 * b]) for b in range(B)])
+    t = table.to(torch.int32).cuda()
+    lens = [blocks * 16 - 9, blocks * 16, 500]
+    qkv = synth.normal_bf16((B, 16 * blocks, (Hq + 2 * Hkv) * d), 3, "cuda")
+    q, k, v = [x.unflatten(-1, (-1, d)) for x in qkv.split([Hq * d, Hkv * d, Hkv * d], dim=-1)]
+    k[:, :16 * shared_blocks], v[:, :16 * shared_blocks] = k[0, :16 * shared_blocks].clone(), v[0, :16 * shared_blocks].clone()
+    rope, at = kv.rope_table(16 * blocks, d), to_dev_i32([0] * B)
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    q_out = torch.empty(B, 16 * blocks, Hq, d, dtype=torch.bfloat16, device="cuda")
+    append = kv.kv_append_norm_rope_fp8 if fp8 else kv.kv_append_norm_rope
+    append(*pools, q, k, v, q_out, *scales, rope, at, page_table=t, q_weight=w, k_weight=w)
+    got = [pool[t[b].long()].flatten(0, 1) for pool in pools for b in range(B)]
+    if fp8:
+        got = [torch.as_tensor(ofp8.e4m3_decode(x.cpu().numpy()), device="cuda") * s.double()[:, None]
+               for x, s in zip(got, [scales[0]] * B + [scales[1]] * B)]
+    else:
+        assert all(torch.equal(x, v[b]) for b, x in enumerate(got[B:]))
+        kr = serving.norm_rotate(f64(k), np.ones(d), 1e-6, np.tile(np.arange(16 * blocks), (B, 1)), d)
+        assert all(np.abs(f64(x) - kr[b]).max() <= (2.0 ** -8 + 2.0 ** -16) * np.abs(kr[b]).max()
+                   for b, x in enumerate(got[:B]))
+    ks, vs = ([x[:L] for x, L in zip(side, lens)] for side in (got[:B], got[B:]))
+    n, p = to_dev_i32(lens), t[0, :shared_blocks].contiguous()
+    qd = q_out[:, -1:].contiguous()
+    o, lse = outputs(B, 1, Hq, d)
+    fn = kv.attn_decode_window_fp8 if fp8 else kv.attn_decode_window
+    fn(qd, *pools, *scales, n, o, 200, 4, lse=lse, page_table=t)
+    check(o, lse, attention64(qd, ks, vs, lens, 200, 4), fp8, what="window")
+    for num_splits in (0, 2):
+        o, lse = outputs(B, 1, Hq, d)
+        shared(qd, pools, scales, n, t, p, o, lse, num_splits=num_splits)
+        check(o, lse, attention64(qd, ks, vs, lens), fp8, what="shared")
+    if not fp8:
+        qc = q_out[:, -T:].contiguous()
+        o, lse = outputs(B, T, Hq, d)
+        kv.attn_prefill_cache_window(qc, *pools, n, o, 200, 4, lse=lse, page_table=t)
+        check(o, lse, attention64(qc, ks, vs, lens, 200, 4), what="chunk")
+
+
+def test_rows_far_into_a_large_contiguous_cache():
+    """The same for a contiguous cache of more than 2^31 elements."""
+    B, Hq, Hkv, d, cap = 2, 16, 8, 128, (1 << 20) + 64
+    kc, vc = (torch.zeros(B, cap, Hkv, d, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    lens = [cap - 20, cap]
+    k, v = (synth.normal_bf16((B, 2000, Hkv, d), s, "cuda") for s in (1, 2))
+    q = synth.normal_bf16((B, 2000, Hq, d), 3, "cuda")
+    start = [L - 2000 for L in lens]
+    q_out, w = torch.empty_like(q), torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    rope = kv.rope_table(cap, d)
+    kv.kv_append_norm_rope(kc, vc, q, k, v, q_out, rope, to_dev_i32(start), q_weight=w, k_weight=w)
+    pos = np.asarray(start)[:, None] + np.arange(2000)
+    kr = serving.norm_rotate(f64(k), np.ones(d), 1e-6, pos, d)
+    n = to_dev_i32(lens)
+    for b in range(B):
+        x = f64(kc[b, start[b]:lens[b]])
+        assert np.abs(x - kr[b]).max() <= (2.0 ** -8 + 2.0 ** -16) * np.abs(kr[b]).max()
+        assert torch.equal(vc[b, start[b]:lens[b]], v[b])
+    for T, call in ((1, kv.attn_decode_window), (8, kv.attn_decode_window), (300, kv.attn_prefill_cache_window)):
+        qt = q_out[:, -T:].contiguous()
+        o, lse = outputs(B, T, Hq, d)
+        call(qt, kc, vc, n, o, 900, 0, lse=lse)
+        # the last 2000 positions stand for the sequence: the window does not reach past them
+        ref = attention64(qt, [kc[b, start[b]:lens[b]] for b in range(B)], [vc[b, start[b]:lens[b]] for b in range(B)],
+                          [2000] * B, 900, 0)
+        check(o, lse, ref, what=f"T={T}")
