@@ -333,3 +333,96 @@ def test_items_of_one_query_tile_follow_one_another():
         kv.attn_prefill_window(q, k, v, o, 300, 4, stream=b)
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+def test_the_first_cuda_call_of_a_host_thread():
+    """A thread that has not used the device has no context of it yet; each call works as its first one."""
+    import threading
+
+    d = 128
+    q, k, v = synth.prefill_inputs(2, 16, 2, 300, d, seed=1, device="cuda")
+    case = synth.decode_inputs(3, 4, 16, 2, d, 0, 0, seed=2, device="cuda", paged=True, lengths=[100, 900, 2500])
+    fp8 = synth.decode_inputs(3, 1, 16, 2, d, 0, 0, seed=3, device="cuda", paged=True, lengths=[100, 900, 2500], fp8=True)
+    n, n8 = to_dev_i32([104, 904, 2504]), to_dev_i32([101, 901, 2501])
+    t, t8 = to_dev_i32(case.page_table), to_dev_i32(fp8.page_table)
+    t[:, :4] = t[0, :4].clone()
+    bf, e4 = (case.q, case.k_pool, case.v_pool), (fp8.q, fp8.k_pool, fp8.v_pool)
+    scales = [torch.as_tensor(s, device="cuda") for s in (fp8.k_scale, fp8.v_scale)]
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    calls = [
+        (q, lambda o: kv.attn_prefill(q, k, v, o)),
+        (q, lambda o: kv.attn_prefill_window(q, k, v, o, 100, 4)),
+        (case.q, lambda o: kv.attn_prefill_cache(*bf, n, o, page_table=t)),
+        (case.q, lambda o: kv.attn_decode(*bf, n, o, page_table=t, workspace=ws)),
+        (fp8.q, lambda o: kv.attn_decode_fp8(*e4, *scales, n8, o, page_table=t8, workspace=ws)),
+        (case.q, lambda o: kv.attn_decode_window(*bf, n, o, 700, 4, page_table=t, workspace=ws)),
+        (fp8.q, lambda o: kv.attn_decode_window_fp8(*e4, *scales, n8, o, 700, 4, page_table=t8, workspace=ws)),
+        (case.q, lambda o: kv.attn_decode_shared(*bf, n, t, t[0, :4], o, workspace=ws)),
+    ]
+    for like, call in calls:
+        want, got = (torch.full_like(like, float("nan"), dtype=torch.float32) for _ in range(2))
+        call(want)
+        torch.cuda.synchronize()
+        failed = []
+
+        def work():
+            try:
+                call(got)
+            except Exception as e:
+                failed.append(e)
+
+        th = threading.Thread(target=work)
+        th.start()
+        th.join()
+        torch.cuda.synchronize()
+        assert not failed and torch.equal(got, want)
+
+
+def test_calls_from_several_host_threads():
+    """Four threads, each on a stream of its own, without workspaces: each gets what it gets alone."""
+    import threading
+
+    Hq, Hkv, d = 16, 2, 128
+    cases, wants = [], []
+    for i in range(4):
+        q, k, v = synth.prefill_inputs(2, Hq, Hkv, 500 + 40 * i, d, seed=i, device="cuda")
+        case = synth.decode_inputs(3, 1 + 3 * i, Hq, Hkv, d, 0, 0, seed=10 + i, device="cuda", paged=True,
+                                   lengths=[100, 900, 2500 + i])
+        n, t = to_dev_i32([L + 1 + 3 * i for L in (100, 900, 2500 + i)]), to_dev_i32(case.page_table)
+        cases.append((q, k, v, case, n, t))
+
+    def run(i, stream, outs):
+        q, k, v, case, n, t = cases[i]
+        kv.attn_prefill_window(q, k, v, outs[0], 100, 4, stream=stream)
+        kv.attn_prefill(q, k, v, outs[1], stream=stream)
+        kv.attn_decode_window(case.q, case.k_pool, case.v_pool, n, outs[2], 700, 4, page_table=t, stream=stream)
+        kv.attn_decode(case.q, case.k_pool, case.v_pool, n, outs[3], page_table=t, stream=stream)
+
+    def outputs(i):
+        return [torch.full_like(x, float("nan"), dtype=torch.float32) for x in (cases[i][0],) * 2 + (cases[i][3].q,) * 2]
+
+    for i in range(4):
+        wants.append(outputs(i))
+        run(i, None, wants[i])
+    torch.cuda.synchronize()
+    got, failed = [[outputs(i) for _ in range(10)] for i in range(4)], []
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            for outs in got[i]:
+                run(i, s, outs)
+            s.synchronize()
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not failed
+    for i in range(4):
+        for outs in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(outs, wants[i]))
