@@ -384,7 +384,8 @@ ATTN_API int rope_table_fill(float* table, int rows, int rot_dim, double theta, 
  *   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)
  * for the rot_dim / 2 pairs (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) with
  * interleaved = 1; elements from rot_dim on are not rotated.  fp32 arithmetic,
- * rounded once.
+ * rounded once (the mean too: values whose squares overflow it, from about 1e19 on,
+ * normalise to 0).
  *
  *   q, k         device bf16, the rows of B * T tokens: Hq (Hkv) * d contiguous
  *                values every q_stride (k_stride) elements, so views of a fused
